@@ -1,4 +1,6 @@
-"""Gated DeltaNet-2 operator on B200: Python binding of libgdn2.so.
+"""Gated DeltaNet-2 operator, and the other operators of its hybrid block (windowed
+attention with sinks, gated linear recurrence, block norm), on B200: Python binding
+of libgdn2.so.
 
 The binding only marshals torch tensors (device memory) and the current CUDA
 stream into the C ABI declared in ``include/gdn2.h``; every step of the
@@ -8,6 +10,7 @@ native library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import torch
@@ -35,10 +38,14 @@ GDN2_ERASE_SCALAR = 1
 GDN2_WRITE_SCALAR = 2
 GDN2_DECAY_SCALAR = 4
 
+# tokens between the checkpoints gdn2_scan_fwd leaves for gdn2_scan_bwd
+GDN2_SCAN_BLOCK = 16
+
 # Every symbol include/gdn2.h declares.
 EXPORTED = ("gdn2_fwd_chunked", "gdn2_fwd_chunked_gates", "gdn2_fwd_chunked_noalloc",
-            "gdn2_layer_fwd", "gdn2_bwd_chunked", "gdn2_decode_step", "gdn2_decode_tokens", "gdn2_check_device_error",
-            "gdn2_selftest_bounded_wait", "gdn2_fwd_chunked_launches", "gdn2_status_string")
+            "gdn2_layer_fwd", "gdn2_bwd_chunked", "gdn2_decode_step", "gdn2_decode_tokens",
+            "gdn2_swa_fwd", "gdn2_swa_bwd", "gdn2_swa_decode", "gdn2_scan_fwd", "gdn2_scan_bwd", "gdn2_scan_step",
+            "gdn2_block_norm_fwd", "gdn2_block_norm_bwd", "gdn2_check_device_error", "gdn2_selftest_bounded_wait", "gdn2_fwd_chunked_launches", "gdn2_status_string")
 
 _lib = None
 
@@ -72,6 +79,18 @@ def lib() -> ctypes.CDLL:
         L.gdn2_fwd_chunked_noalloc.restype = ci
         L.gdn2_decode_step.argtypes = [vp] * 5 + [fp, fp, vp] + [ci] * 5 + [vp]
         L.gdn2_decode_step.restype = ci
+        cl, cf = ctypes.c_longlong, ctypes.c_float
+        L.gdn2_swa_fwd.argtypes = [vp] * 6 + [ci] * 8 + [cf, vp, ci, vp]
+        L.gdn2_swa_bwd.argtypes = [vp] * 10 + [ci] * 8 + [cf, vp, ci, vp]
+        L.gdn2_swa_decode.argtypes = [vp] * 7 + [ci] * 7 + [cf, vp, ci, vp]
+        L.gdn2_scan_fwd.argtypes = [vp] * 7 + [ci] * 4 + [vp]
+        L.gdn2_scan_bwd.argtypes = [vp] * 10 + [ci] * 4 + [vp]
+        L.gdn2_scan_step.argtypes = [vp] * 5 + [ci] * 3 + [vp]
+        L.gdn2_block_norm_fwd.argtypes = [vp] * 6 + [cf] + [vp] * 2 + [cl, ci, ci, vp]
+        L.gdn2_block_norm_bwd.argtypes = [vp] * 6 + [cf] + [vp] * 8 + [cl, ci, ci, vp]
+        for fn in (L.gdn2_swa_fwd, L.gdn2_swa_bwd, L.gdn2_swa_decode, L.gdn2_scan_fwd, L.gdn2_scan_bwd,
+                   L.gdn2_scan_step, L.gdn2_block_norm_fwd, L.gdn2_block_norm_bwd):
+            fn.restype = ci
         L.gdn2_check_device_error.argtypes = [vp]
         L.gdn2_check_device_error.restype = ci
         L.gdn2_selftest_bounded_wait.argtypes = [vp]
@@ -254,6 +273,265 @@ def gdn2_decode_tokens(q, k, v, b, w, log_alpha, S, o=None, *, stream=None, chec
     if check and st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_decode_tokens")
     return o
+
+
+# ---------------------------------------------------------------- the hybrid block's other operators
+def _on_device(fn):
+    """Runs ``fn`` with the first tensor's device current, on ``stream`` if one is given (outputs are
+    then allocated for that stream too), else on that device's current stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not (isinstance(first, torch.Tensor) and first.is_cuda):
+            raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError(f"{fn.__name__}: stream is on {stream.device}, tensors on {first.device}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need(name, t, shape, dtype, device, dense=True):
+    """``t`` is a tensor of this shape, type and device (None passes)."""
+    if t is None:
+        return
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if dense:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    elif t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _done(st, check, where):
+    if check and st != GDN2_OK:
+        raise Gdn2Error(st, where)
+
+
+def _strides(q, k, v):
+    """Host array of the strides of all axes but the last; None if all three are dense."""
+    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+        return None
+    st = [*q.stride()[:-1], *k.stride()[:-1], *v.stride()[:-1]]
+    return (ctypes.c_longlong * len(st))(*st)
+
+
+def _swa_sizes(q, k, v, lens, window, sinks, scale):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,T,Hq,d], k and v [B,Tk,Hk,d]")
+    B, T, Hq, d = q.shape
+    Tk, Hk = k.shape[1], k.shape[2]
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(q)
+    _need("q", q, q.shape, dt, dev, dense=False)
+    _need("k", k, (B, Tk, Hk, d), dt, dev, dense=False)
+    _need("v", v, (B, Tk, Hk, d), dt, dev, dense=False)
+    _need("lens", lens, (B,), torch.int32, dev)
+    scale = d ** -0.5 if scale is None else float(scale)
+    return (B, T, Tk, Hq, Hk, d, int(window), int(sinks), scale, _strides(q, k, v), code, _raw_stream(dev))
+
+
+@_on_device
+def gdn2_swa_fwd(q, k, v, lens=None, o=None, lse=None, *, window, sinks=0, scale=None, want_lse=True, check=True):
+    """Causal attention over a sliding window and ``sinks`` first tokens.  q [B,T,Hq,d], k and v
+    [B,Tk,Hk,d] (Tk >= T; the queries are the last T positions), which may be strided views with
+    contiguous rows, such as slices of one packed projection; ``lens`` [B] int32 or None; ``scale``
+    defaults to d ** -0.5.  Also takes ``stream``.  Returns (o, lse), lse [B,Hq,T] fp32 or None
+    unless ``want_lse``."""
+    args = _swa_sizes(q, k, v, lens, window, sinks, scale)
+    B, T, Hq, d = q.shape
+    if o is None:
+        o = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device)
+    else:
+        _need("o", o, q.shape, q.dtype, q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if want_lse else None
+    else:
+        _need("lse", lse, (B, Hq, T), torch.float32, q.device)
+    st = lib().gdn2_swa_fwd(_p(q), _p(k), _p(v), _p(lens), _p(o), _p(lse), *args)
+    _done(st, check, "gdn2_swa_fwd")
+    return o, lse
+
+
+@_on_device
+def gdn2_swa_bwd(q, k, v, o, lse, dO, lens=None, *, window, sinks=0, scale=None, check=True):
+    """Backward of gdn2_swa_fwd from its inputs, its o and lse, and dO [B,T,Hq,d]; returns a dict
+    of dq, dk and dv (dense, in the inputs' dtype).  Also takes ``stream``."""
+    args = _swa_sizes(q, k, v, lens, window, sinks, scale)
+    B, T, Hq, d = q.shape
+    _need("o", o, q.shape, q.dtype, q.device)
+    _need("dO", dO, q.shape, q.dtype, q.device)
+    _need("lse", lse, (B, Hq, T), torch.float32, q.device)
+    g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    st = lib().gdn2_swa_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(dO), _p(lens), _p(g["dq"]), _p(g["dk"]),
+                            _p(g["dv"]), *args)
+    _done(st, check, "gdn2_swa_bwd")
+    return g
+
+
+@_on_device
+def gdn2_swa_decode(q, k, v, k_cache, v_cache, pos, o=None, *, window, sinks=0, scale=None, check=True):
+    """One token per sequence against a ring cache: q [B,Hq,d], new k and v [B,Hk,d] (all three may
+    be strided views with contiguous rows), k_cache and v_cache [B,slots,Hk,d] updated in place, pos
+    [B] int32 the new token's position (< 0: no sequence in this row).  Position p lives in slot p if
+    p < sinks, else in slot sinks + (p - sinks) % (slots - sinks).  Also takes ``stream``.  Returns o."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [B,Hq,d], the caches [B,slots,Hk,d]")
+    B, Hq, d = q.shape
+    slots, Hk = k_cache.shape[1], k_cache.shape[2]
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(q)
+    _need("q", q, q.shape, dt, dev, dense=False)
+    _need("k", k, (B, Hk, d), dt, dev, dense=False)
+    _need("v", v, (B, Hk, d), dt, dev, dense=False)
+    _need("k_cache", k_cache, (B, slots, Hk, d), dt, dev)
+    _need("v_cache", v_cache, (B, slots, Hk, d), dt, dev)
+    _need("pos", pos, (B,), torch.int32, dev)
+    if o is None:
+        o = torch.empty((B, Hq, d), dtype=dt, device=dev)
+    else:
+        _need("o", o, q.shape, dt, dev)
+    st = lib().gdn2_swa_decode(_p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(pos), _p(o), B, slots, Hq, Hk, d,
+                               int(window), int(sinks), d ** -0.5 if scale is None else float(scale),
+                               _strides(q, k, v), code, _raw_stream(dev))
+    _done(st, check, "gdn2_swa_decode")
+    return o
+
+
+@_on_device
+def gdn2_scan_fwd(x, w, log_alpha, h0=None, y=None, h_T=None, *, want_state=True, want_ckpt=False, check=True):
+    """Gated linear recurrence h_t = exp(log_alpha_t) h_{t-1} + w_t x_t per channel: x, w [B,T,C],
+    log_alpha [B,T,C] fp32, h0 [B,C] fp32 or None.  Also takes ``stream``.  Returns (y, h_T), and with
+    ``want_ckpt`` (y, h_T, ckpt), ckpt being what gdn2_scan_bwd needs."""
+    B, T, C = x.shape
+    dev = x.device
+    code = _dtype_code(x)
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("w", w, x.shape, x.dtype, dev)
+    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
+    _need("h0", h0, (B, C), torch.float32, dev)
+    _need("y", y, x.shape, x.dtype, dev)
+    _need("h_T", h_T, (B, C), torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+    if h_T is None and want_state:
+        h_T = torch.empty((B, C), dtype=torch.float32, device=dev)
+    ckpt = None
+    if want_ckpt:
+        ckpt = torch.empty((B, -(-T // GDN2_SCAN_BLOCK), C), dtype=torch.float32, device=dev)
+    st = lib().gdn2_scan_fwd(_p(x), _p(w), _p(log_alpha), _p(h0), _p(y), _p(h_T), _p(ckpt), B, T, C, code,
+                             _raw_stream(dev))
+    _done(st, check, "gdn2_scan_fwd")
+    return (y, h_T, ckpt) if want_ckpt else (y, h_T)
+
+
+@_on_device
+def gdn2_scan_bwd(x, w, log_alpha, ckpt, dy, dh_T=None, *, want_dh0=True, check=True):
+    """Backward of gdn2_scan_fwd: its inputs and ckpt, dy [B,T,C] and dh_T [B,C] fp32 or None.  Also
+    takes ``stream``.  Returns a dict of dx, dw (inputs' dtype), dlog_alpha and dh0 (fp32; dh0 None
+    unless ``want_dh0``)."""
+    B, T, C = x.shape
+    dev = x.device
+    code = _dtype_code(x)
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("w", w, x.shape, x.dtype, dev)
+    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
+    _need("ckpt", ckpt, (B, -(-T // GDN2_SCAN_BLOCK), C), torch.float32, dev)
+    _need("dy", dy, x.shape, x.dtype, dev)
+    _need("dh_T", dh_T, (B, C), torch.float32, dev)
+    g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
+         "dw": torch.empty((B, T, C), dtype=x.dtype, device=dev),
+         "dlog_alpha": torch.empty((B, T, C), dtype=torch.float32, device=dev),
+         "dh0": torch.empty((B, C), dtype=torch.float32, device=dev) if want_dh0 else None}
+    st = lib().gdn2_scan_bwd(_p(x), _p(w), _p(log_alpha), _p(ckpt), _p(dy), _p(dh_T), _p(g["dx"]), _p(g["dw"]),
+                             _p(g["dlog_alpha"]), _p(g["dh0"]), B, T, C, code, _raw_stream(dev))
+    _done(st, check, "gdn2_scan_bwd")
+    return g
+
+
+@_on_device
+def gdn2_scan_step(x, w, log_alpha, h, y=None, *, check=True):
+    """One token of the recurrence: x, w [B,C], log_alpha and h [B,C] fp32, h updated in place.
+    Also takes ``stream``.  Returns y."""
+    B, C = x.shape
+    dev = x.device
+    code = _dtype_code(x)
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("w", w, x.shape, x.dtype, dev)
+    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
+    _need("h", h, x.shape, torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+    else:
+        _need("y", y, x.shape, x.dtype, dev)
+    st = lib().gdn2_scan_step(_p(x), _p(w), _p(log_alpha), _p(h), _p(y), B, C, code, _raw_stream(dev))
+    _done(st, check, "gdn2_scan_step")
+    return y
+
+
+def _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre):
+    D, dev = r.shape[-1], r.device
+    _need("r", r, r.shape, r.dtype, dev)
+    _need("y", y, r.shape, r.dtype, dev)
+    _need("g_logit", g_logit, r.shape, r.dtype, dev)
+    for name, t in (("w_post", w_post), ("res_scale", res_scale), ("w_pre", w_pre)):
+        _need(name, t, (D,), torch.float32, dev)
+    return r.numel() // D if D else 0, D, _dtype_code(r)
+
+
+@_on_device
+def gdn2_block_norm_fwd(r, y, g_logit, w_post, res_scale, w_pre, eps=1e-6, r_out=None, x_out=None, *, check=True):
+    """The norms around a block: r_out = r + res_scale * sigmoid(g_logit) * RMSNorm(y) * w_post and
+    x_out = RMSNorm(r_out) * w_pre, over the last axis (r, y, g_logit of one shape; g_logit None: no
+    gate; the three vectors fp32).  r_out may be r.  Also takes ``stream``.  Returns (r_out, x_out)."""
+    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre)
+    _need("r_out", r_out, r.shape, r.dtype, r.device)
+    _need("x_out", x_out, r.shape, r.dtype, r.device)
+    if r_out is None:
+        r_out = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    if x_out is None:
+        x_out = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    st = lib().gdn2_block_norm_fwd(_p(r), _p(y), _p(g_logit), _p(w_post), _p(res_scale), _p(w_pre), float(eps),
+                                   _p(r_out), _p(x_out), N, D, code, _raw_stream(r.device))
+    _done(st, check, "gdn2_block_norm_fwd")
+    return r_out, x_out
+
+
+@_on_device
+def gdn2_block_norm_bwd(r, y, g_logit, w_post, res_scale, w_pre, dr_out, dx_out, eps=1e-6, *, check=True):
+    """Backward of gdn2_block_norm_fwd from its inputs and the gradients of r_out and x_out.  Also
+    takes ``stream``.  Returns a dict of dr, dy, dg_logit (inputs' dtype; dg_logit None without a
+    gate), dw_post, dres_scale and dw_pre (fp32)."""
+    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre)
+    _need("dr_out", dr_out, r.shape, r.dtype, r.device)
+    _need("dx_out", dx_out, r.shape, r.dtype, r.device)
+    like = dict(dtype=r.dtype, device=r.device)
+    g = {"dr": torch.empty(r.shape, **like), "dy": torch.empty(r.shape, **like),
+         "dg_logit": None if g_logit is None else torch.empty(r.shape, **like)}
+    g.update({n: torch.empty((D,), dtype=torch.float32, device=r.device) for n in ("dw_post", "dres_scale", "dw_pre")})
+    st = lib().gdn2_block_norm_bwd(_p(r), _p(y), _p(g_logit), _p(w_post), _p(res_scale), _p(w_pre), float(eps),
+                                   _p(dr_out), _p(dx_out), _p(g["dr"]), _p(g["dy"]), _p(g["dg_logit"]),
+                                   _p(g["dw_post"]), _p(g["dres_scale"]), _p(g["dw_pre"]), N, D, code,
+                                   _raw_stream(r.device))
+    _done(st, check, "gdn2_block_norm_bwd")
+    return g
 
 
 def gdn2_check_device_error(stream=None) -> int:

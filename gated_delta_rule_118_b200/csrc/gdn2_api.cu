@@ -61,6 +61,9 @@ bool device_error_word(unsigned int **err)
     return device_context(err, &sms) == GDN2_OK;
 }
 
+// The same, and the device's SM count.
+bool device_info(unsigned int **err, int *num_sms) { return device_context(err, num_sms) == GDN2_OK; }
+
 }  // namespace gdn2
 
 using namespace gdn2;

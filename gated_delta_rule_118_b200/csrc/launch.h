@@ -69,6 +69,7 @@ cudaError_t launch_bwd_tc(const BwdArgs &a, uint8_t *ws, unsigned int *err, int 
 cudaMemPool_t workspace_pool(int dev);
 
 bool device_error_word(unsigned int **err);
+bool device_info(unsigned int **err, int *num_sms);
 cudaError_t launch_decode(const DecodeArgs &a);
 cudaError_t launch_fwd_simt(const FwdArgs &a);
 

@@ -1,0 +1,400 @@
+// swa_simt.cu -- windowed attention in fp32 on the CUDA cores: forward, and the
+// backward as two kernels without atomics (dq by query tiles; dk and dv by key
+// tiles).  The products are 64-wide register tiles over shared memory; bound by
+// the FFMA rate (every score costs 2 d FMAs, and the two-kernel backward forms
+// q k^T and dO v^T twice in exchange for a fixed order of every sum).
+#include "swa_common.cuh"
+
+namespace gdn2 {
+namespace {
+
+using namespace swa;
+
+constexpr int kThreads = 256;  // 16 x 16: ty = query (or key) rows, tx = columns
+
+// Rows [r0, r0 + N) of `src` into shared memory (row stride D + 4), zeros from row `end` on.
+template <typename E, int D, int N>
+__device__ __forceinline__ void load_rows(float *dst, const Rows<E> &src, int r0, int end)
+{
+    for (int c = threadIdx.x; c < N * D / 4; c += kThreads) {
+        const int r = c / (D / 4), x = c % (D / 4) * 4;
+        const float4 f = r0 + r < end ? load4(src[r0 + r] + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + x) = f;
+    }
+}
+
+// s[i][j] += A[ra + i] . B[cb + 16 j] over D.
+template <int D, int NI, int NJ>
+__device__ __forceinline__ void dot_tile(float (&s)[NI][NJ], const float *A, int ra, const float *B, int cb)
+{
+#pragma unroll 4
+    for (int x = 0; x < D; x += 4) {
+        float4 u[NI], w[NJ];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) u[i] = *reinterpret_cast<const float4 *>(A + (ra + i) * (D + 4) + x);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) w[j] = *reinterpret_cast<const float4 *>(B + (cb + 16 * j) * (D + 4) + x);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                s[i][j] = fmaf(u[i].x, w[j].x, fmaf(u[i].y, w[j].y, fmaf(u[i].z, w[j].z, fmaf(u[i].w, w[j].w, s[i][j]))));
+    }
+}
+
+// acc[i][c] += sum_j P[ra + i][j] V[j][cols of tx], NK rows of V, P with row stride PS.
+template <int D, int NK, int PS>
+__device__ __forceinline__ void mul_tile(float (&acc)[4][D / 16], const float *P, int ra, const float *V, int tx)
+{
+#pragma unroll 2
+    for (int j = 0; j < NK; j += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (ra + i) * PS + j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float4 v = *reinterpret_cast<const float4 *>(V + (j + r) * (D + 4) + tx * 4 + 64 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = r == 0 ? p[i].x : r == 1 ? p[i].y : r == 2 ? p[i].z : p[i].w;
+                    acc[i][4 * c] = fmaf(w, v.x, acc[i][4 * c]);
+                    acc[i][4 * c + 1] = fmaf(w, v.y, acc[i][4 * c + 1]);
+                    acc[i][4 * c + 2] = fmaf(w, v.z, acc[i][4 * c + 2]);
+                    acc[i][4 * c + 3] = fmaf(w, v.w, acc[i][4 * c + 3]);
+                }
+            }
+    }
+}
+
+// acc[i][c] += sum_r P[r][ka + i] Q[r][cols of tx], NR rows, P with row stride PS.
+template <int D, int NR, int PS>
+__device__ __forceinline__ void mul_tile_t(float (&acc)[4][D / 16], const float *P, int ka, const float *Q, int tx)
+{
+#pragma unroll 4
+    for (int r = 0; r < NR; ++r) {
+        const float4 p = *reinterpret_cast<const float4 *>(P + r * PS + ka);
+        const float w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 v = *reinterpret_cast<const float4 *>(Q + r * (D + 4) + tx * 4 + 64 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][4 * c] = fmaf(w[i], v.x, acc[i][4 * c]);
+                acc[i][4 * c + 1] = fmaf(w[i], v.y, acc[i][4 * c + 1]);
+                acc[i][4 * c + 2] = fmaf(w[i], v.z, acc[i][4 * c + 2]);
+                acc[i][4 * c + 3] = fmaf(w[i], v.w, acc[i][4 * c + 3]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float max16(float x)
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+    return x;
+}
+__device__ __forceinline__ float sum16(float x)
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Writes row `t` (columns of tx) scaled by f; true if any of them is not finite.
+template <typename E, int D>
+__device__ __forceinline__ bool store_cols(E *dst, const float (&acc)[D / 16], float f, int tx)
+{
+    bool bad = false;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const float4 v = make_float4(acc[4 * c] * f, acc[4 * c + 1] * f, acc[4 * c + 2] * f, acc[4 * c + 3] * f);
+        bad |= !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w));
+        store4(dst + tx * 4 + 64 * c, v);
+    }
+    return bad;
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
+{
+    constexpr int LD = D + 4, PS = 68;
+    extern __shared__ float sm[];
+    float *Qs = sm, *KV = Qs + 64 * LD, *Ps = KV + 64 * LD;
+    __shared__ unsigned bad[2];
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int i0 = (gridDim.x - 1 - blockIdx.x) * 64, h = blockIdx.y, b = blockIdx.z;  // longest rows first
+    const int n = seq_len(a, b), off = a.Tk - a.T, hk = h / (a.Hq / a.Hk);
+    const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), k = rows_of<E>(a.k, a.ks, b, hk), v = rows_of<E>(a.v, a.vs, b, hk);
+    E *out = const_cast<E *>(dense_rows<E>(a.out, b, h, a.T, a.Hq, D)[0]);
+    const long long ost = (long long)a.Hq * D, lrow = ((long long)b * a.Hq + h) * a.T;
+    if (tid < 2) bad[tid] = 0;
+    float o[4][D / 16] = {}, m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    if (i0 < n) {
+        load_rows<E, D, 64>(Qs, q, i0, n);
+        const int p0 = off + i0, p1 = off + min(i0 + 64, n) - 1;
+        const KeyTiles kt(p0, p1, a.window, a.sinks, 64);
+        for (int c = 0; c < kt.count(); ++c) {
+            const int j0 = kt.tile(c) * 64;
+            __syncthreads();
+            load_rows<E, D, 64>(KV, k, j0, a.Tk);
+            __syncthreads();
+            float s[4][4] = {};
+            dot_tile<D, 4, 4>(s, Qs, ty * 4, KV, tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = sees(p0 + ty * 4 + i, j0 + tx + 16 * j, a.window, a.sinks) ? s[i][j] * (a.scale * kLog2e)
+                                                                                        : -INFINITY;
+                    mx = fmaxf(mx, s[i][j]);
+                }
+                const float mn = fmaxf(m[i], max16(mx)), ms = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[i] - ms);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = exp2f(s[i][j] - ms);
+                    sum += e;
+                    Ps[(ty * 4 + i) * PS + tx + 16 * j] = e;
+                }
+                m[i] = mn;
+                l[i] = l[i] * f + sum16(sum);
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) o[i][u] *= f;
+            }
+            __syncthreads();
+            load_rows<E, D, 64>(KV, v, j0, a.Tk);
+            __syncthreads();
+            mul_tile<D, 64, PS>(o, Ps, ty * 4, KV, tx);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = i0 + ty * 4 + i;
+        if (t >= a.T) continue;
+        const bool live = t < n;
+        if (!live)
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) o[i][u] = 0.f;
+        const float inv = !live || l[i] == 0.f ? 0.f : 1.f / l[i];
+        const bool nf = store_cols<E, D>(out + t * ost, o[i], inv, tx);
+        if (live && nf) atomicOr(&bad[(ty * 4 + i) >> 5], 1u << ((ty * 4 + i) & 31));
+        if (a.lse && tx == 0) a.lse[lrow + t] = !live || l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < 64; r += kThreads / 32)
+        if (bad[r >> 5] >> (r & 31) & 1) row_forward<E, D>(a, b, h, i0 + r);
+}
+
+// dq of 64 query rows, key tiles of 32.
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
+{
+    constexpr int LD = D + 4, PS = 36;
+    extern __shared__ float sm[];
+    float *Qs = sm, *Gs = Qs + 64 * LD, *Ks = Gs + 64 * LD, *Vs = Ks + 32 * LD, *Ps = Vs + 32 * LD;
+    __shared__ unsigned bad[2];
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int i0 = (gridDim.x - 1 - blockIdx.x) * 64, h = blockIdx.y, b = blockIdx.z;
+    const int n = seq_len(a, b), off = a.Tk - a.T, hk = h / (a.Hq / a.Hk);
+    const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), k = rows_of<E>(a.k, a.ks, b, hk), v = rows_of<E>(a.v, a.vs, b, hk);
+    const Rows<E> g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D);
+    E *out = const_cast<E *>(dense_rows<E>(a.dq, b, h, a.T, a.Hq, D)[0]);
+    const long long ost = (long long)a.Hq * D, lrow = ((long long)b * a.Hq + h) * a.T;
+    if (tid < 2) bad[tid] = 0;
+    float acc[4][D / 16] = {}, lse[4], delta[4];
+    if (i0 < n) {
+        load_rows<E, D, 64>(Qs, q, i0, n);
+        load_rows<E, D, 64>(Gs, g, i0, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = min(i0 + ty * 4 + i, n - 1);
+            lse[i] = a.lse[lrow + t];
+            delta[i] = a.delta[lrow + t];
+        }
+        const int p0 = off + i0, p1 = off + min(i0 + 64, n) - 1;
+        const KeyTiles kt(p0, p1, a.window, a.sinks, 32);
+        for (int c = 0; c < kt.count(); ++c) {
+            const int j0 = kt.tile(c) * 32;
+            __syncthreads();
+            load_rows<E, D, 32>(Ks, k, j0, a.Tk);
+            load_rows<E, D, 32>(Vs, v, j0, a.Tk);
+            __syncthreads();
+            float s[4][2] = {}, dp[4][2] = {};
+            dot_tile<D, 4, 2>(s, Qs, ty * 4, Ks, tx);
+            dot_tile<D, 4, 2>(dp, Gs, ty * 4, Vs, tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const bool on = sees(p0 + ty * 4 + i, j0 + tx + 16 * j, a.window, a.sinks);
+                    Ps[(ty * 4 + i) * PS + tx + 16 * j] =
+                        on ? prob(s[i][j], a.scale * kLog2e, lse[i]) * (dp[i][j] - delta[i]) : 0.f;
+                }
+            __syncthreads();
+            mul_tile<D, 32, PS>(acc, Ps, ty * 4, Ks, tx);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = i0 + ty * 4 + i;
+        if (t >= a.T) continue;
+        if (t >= n)
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) acc[i][u] = 0.f;
+        if (store_cols<E, D>(out + t * ost, acc[i], a.scale, tx)) atomicOr(&bad[(ty * 4 + i) >> 5], 1u << ((ty * 4 + i) & 31));
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < 64; r += kThreads / 32)
+        if (bad[r >> 5] >> (r & 31) & 1) row_dq<E, D>(a, b, h, i0 + r);
+}
+
+// dk and dv of 64 keys, query tiles of 32 rows over all heads of the group.
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
+{
+    constexpr int LD = D + 4, PS = 68;
+    extern __shared__ float sm[];
+    float *Ks = sm, *Vs = Ks + 64 * LD, *Qs = Vs + 64 * LD, *Gs = Qs + 32 * LD, *Ps = Gs + 32 * LD;
+    __shared__ unsigned bad[2];
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int j0 = blockIdx.x * 64, hk = blockIdx.y, b = blockIdx.z;
+    const int n = seq_len(a, b), off = a.Tk - a.T, G = a.Hq / a.Hk;
+    if (tid < 2) bad[tid] = 0;
+    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+    load_rows<E, D, 64>(Ks, rows_of<E>(a.k, a.ks, b, hk), j0, a.Tk);
+    load_rows<E, D, 64>(Vs, rows_of<E>(a.v, a.vs, b, hk), j0, a.Tk);
+    const int i_lo = max(j0 - off, 0);
+    const long long far = (long long)min(j0 + 64, a.Tk) - 1 + a.window - off;  // first row behind every window
+    const int i_hi = (j0 < a.sinks || far > n) ? n : (int)far;
+    for (int h = hk * G; h < hk * G + G; ++h) {
+        const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D);
+        const long long lrow = ((long long)b * a.Hq + h) * a.T;
+        for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+            __syncthreads();
+            load_rows<E, D, 32>(Qs, q, i0, n);
+            load_rows<E, D, 32>(Gs, g, i0, n);
+            __syncthreads();
+            float s[2][4] = {}, dp[2][4] = {};
+            dot_tile<D, 2, 4>(s, Qs, ty * 2, Ks, tx);
+            dot_tile<D, 2, 4>(dp, Gs, ty * 2, Vs, tx);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = i0 + ty * 2 + i, tc = min(t, n - 1);
+                const float lse = a.lse[lrow + tc], delta = a.delta[lrow + tc];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool on = t < n && sees(off + t, j0 + tx + 16 * j, a.window, a.sinks);
+                    s[i][j] = on ? prob(s[i][j], a.scale * kLog2e, lse) : 0.f;
+                    dp[i][j] = on ? s[i][j] * (dp[i][j] - delta) : 0.f;
+                    Ps[(ty * 2 + i) * PS + tx + 16 * j] = s[i][j];
+                }
+            }
+            __syncthreads();
+            mul_tile_t<D, 32, PS>(dv, Ps, ty * 4, Gs, tx);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) Ps[(ty * 2 + i) * PS + tx + 16 * j] = dp[i][j];
+            __syncthreads();
+            mul_tile_t<D, 32, PS>(dk, Ps, ty * 4, Qs, tx);
+        }
+    }
+    __syncthreads();
+    E *ok = const_cast<E *>(dense_rows<E>(a.dk, b, hk, a.Tk, a.Hk, D)[0]);
+    E *ov = const_cast<E *>(dense_rows<E>(a.dv, b, hk, a.Tk, a.Hk, D)[0]);
+    const long long st = (long long)a.Hk * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + ty * 4 + i;
+        if (j >= a.Tk) continue;
+        bool nf = store_cols<E, D>(ok + j * st, dk[i], a.scale, tx);
+        nf |= store_cols<E, D>(ov + j * st, dv[i], 1.f, tx);
+        if (nf) atomicOr(&bad[(ty * 4 + i) >> 5], 1u << ((ty * 4 + i) & 31));
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < 64; r += kThreads / 32)
+        if (bad[r >> 5] >> (r & 31) & 1) row_dkdv<E, D>(a, b, hk, j0 + r);
+}
+
+// delta = dO . o of every row that holds a token, one warp per row.
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) delta_kernel(const SwaArgs a)
+{
+    const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (b, t, h)
+    if (row >= (long long)a.B * a.T * a.Hq) return;
+    const int lane = threadIdx.x & 31, h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.T), b = (int)(row / a.Hq / a.T);
+    float s = 0.f;
+    if (t < seq_len(a, b)) {
+        const E *o = static_cast<const E *>(a.o) + row * D, *g = static_cast<const E *>(a.dO) + row * D;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) s = fmaf(to_f32(o[lane + 32 * u]), to_f32(g[lane + 32 * u]), s);
+        s = warp_sum(s);
+    }
+    if (lane == 0) a.delta[((long long)b * a.Hq + h) * a.T + t] = s;
+}
+
+template <typename E, int D>
+cudaError_t fwd_impl(const SwaArgs &a, cudaStream_t stream)
+{
+    constexpr int bytes = sizeof(float) * (2 * 64 * (D + 4) + 64 * 68);
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    fwd_kernel<E, D><<<dim3((a.T + 63) / 64, a.Hq, a.B), kThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t bwd_impl(const SwaArgs &a, cudaStream_t stream)
+{
+    constexpr int dq_bytes = sizeof(float) * (192 * (D + 4) + 64 * 36), kv_bytes = sizeof(float) * (192 * (D + 4) + 32 * 68);
+    cudaError_t e = cudaFuncSetAttribute(dq_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dkdv_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
+    if (e != cudaSuccess) return e;
+    dq_kernel<E, D><<<dim3((a.T + 63) / 64, a.Hq, a.B), kThreads, dq_bytes, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    dkdv_kernel<E, D><<<dim3((a.Tk + 63) / 64, a.Hk, a.B), kThreads, kv_bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t delta_impl(const SwaArgs &a, cudaStream_t stream)
+{
+    const long long rows = (long long)a.B * a.T * a.Hq, blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    delta_kernel<E, D><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_swa_fwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream)
+{
+    if (bf16) return a.d == 128 ? fwd_impl<__nv_bfloat16, 128>(a, stream) : fwd_impl<__nv_bfloat16, 64>(a, stream);
+    return a.d == 128 ? fwd_impl<float, 128>(a, stream) : fwd_impl<float, 64>(a, stream);
+}
+
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream)
+{
+    if (bf16) return a.d == 128 ? bwd_impl<__nv_bfloat16, 128>(a, stream) : bwd_impl<__nv_bfloat16, 64>(a, stream);
+    return a.d == 128 ? bwd_impl<float, 128>(a, stream) : bwd_impl<float, 64>(a, stream);
+}
+
+cudaError_t launch_swa_delta(const SwaArgs &a, bool bf16, cudaStream_t stream)
+{
+    if (bf16) return a.d == 128 ? delta_impl<__nv_bfloat16, 128>(a, stream) : delta_impl<__nv_bfloat16, 64>(a, stream);
+    return a.d == 128 ? delta_impl<float, 128>(a, stream) : delta_impl<float, 64>(a, stream);
+}
+
+}  // namespace gdn2

@@ -303,6 +303,186 @@ gdn2_status gdn2_bwd_chunked(const void *q, const void *k, const void *v,
                              gdn2_dtype dtype, gdn2_stream_t stream);
 
 /*
+ * ======================================================================
+ * The other operators of a hybrid block: windowed attention with sinks, a
+ * diagonal gated linear recurrence, and the norms around a block.  The pages'
+ * hybrid model interleaves the operator above with attention over a window of
+ * 2K tokens (iplexlaw.co.kr, section "Condiciones de comparacion"; gist.science,
+ * architecture).  They follow the conventions at the top of this header, with
+ * one addition: the gradient of an input has the input's own type.
+ * ======================================================================
+ */
+
+/*
+ * gdn2_swa_fwd -- causal attention over a sliding window and a few first tokens
+ * that stay visible (sinks), forward over T query tokens.
+ *
+ * The T queries are the last T of Tk positions: query i stands at position
+ * p = Tk - T + i (Tk = T for a whole sequence; Tk > T continues a sequence whose
+ * earlier keys are at the front of k and v).  Key j is visible to position p iff
+ *     j <= p   and   (p - j < window   or   j < sinks)
+ * and, over the visible keys of row i,
+ *     o_i = sum_j softmax_j(scale * q_i . k_j) v_j,
+ *     lse_i = log sum_j exp(scale * q_i . k_j).
+ * Query head h reads key/value head h / (Hq / Hk).
+ *
+ *   q           [B][T][Hq][d]   dtype
+ *   k, v        [B][Tk][Hk][d]  dtype
+ *   lens        [B]             int32, device; NULL means T everywhere.  Sequence b
+ *               has lens[b] query rows (cut to 0..T); the rows behind them are
+ *               padding: o = 0, lse = -infinity.
+ *   o           [B][T][Hq][d]   dtype  written
+ *   lse         [B][Hq][T]      fp32   written; NULL means not wanted (the backward
+ *               needs it)
+ *   strides     host array of 9 element strides, {batch, token, head} of q, then of
+ *               k, then of v; NULL means dense.  The d elements of a row are always
+ *               contiguous; a stride is a multiple of 16 bytes and at least d.
+ *               Strides of an axis of size 1 are ignored.
+ *   d 64 or 128; Hq a multiple of Hk; 0 <= T <= Tk; window >= 1; 0 <= sinks;
+ *   scale > 0 and finite.
+ *
+ * A row whose visible scores are all -infinity gives o = 0 and lse = -infinity.
+ * What stands in places that a row does not see (keys behind the window or ahead
+ * of the row, padding) never reaches that row, infinities and NaN included.
+ * bf16 inputs run on the tensor cores (fp32 scores, statistics and sums; the
+ * probabilities rounded to bf16 for the product with v); fp32 inputs in fp32 on
+ * the CUDA cores.
+ */
+gdn2_status gdn2_swa_fwd(const void *q, const void *k, const void *v, const int *lens, void *o, float *lse,
+                         int B, int T, int Tk, int Hq, int Hk, int d, int window, int sinks, float scale,
+                         const long long *strides, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_swa_bwd -- gradients of sum(o * dO) with respect to q, k and v, from the
+ * forward's o and lse.  With P the probabilities and D_i = dO_i . o_i,
+ *     dv_j = sum_i P_ij dO_i,   dS_ij = P_ij (dO_i . v_j - D_i),
+ *     dq_i = scale * sum_j dS_ij k_j,   dk_j = scale * sum_i dS_ij q_i,
+ * sums over i running over the query heads of the group too.
+ *
+ *   q, k, v, lens, strides, sizes   as for gdn2_swa_fwd
+ *   o, dO       [B][T][Hq][d]   dtype  dense
+ *   lse         [B][Hq][T]      fp32   of the forward
+ *   dq          [B][T][Hq][d]   dtype  written (0 in padding rows)
+ *   dk, dv      [B][Tk][Hk][d]  dtype  written (0 where no row sees the key)
+ *
+ * No atomics: repeated calls give identical bits.  Takes its workspace (D, and
+ * the partial sums of the keys that all rows see) from the library's pool.
+ */
+gdn2_status gdn2_swa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                         const void *dO, const int *lens, void *dq, void *dk, void *dv,
+                         int B, int T, int Tk, int Hq, int Hk, int d, int window, int sinks, float scale,
+                         const long long *strides, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_swa_decode -- one token of the windowed attention per sequence, against a
+ * cache of fixed size: `sinks` slots for the first tokens, then a ring for the
+ * window.  Position p lives in slot p if p < sinks, else in slot
+ * sinks + (p - sinks) % (slots - sinks).
+ *
+ * The call puts k and v into the cache at position pos[b] (as gdn2_decode_step
+ * advances its state in place) and then attends from that position.  pos is not
+ * advanced.  pos[b] < 0 marks a row of the batch without a sequence: its o is 0
+ * and its cache is left as it is.
+ *
+ *   q, o        [B][Hq][d]           dtype  (o written)
+ *   k, v        [B][Hk][d]           dtype  the new token's
+ *   k_cache, v_cache  [B][slots][Hk][d]  dtype  updated in place
+ *   pos         [B]                  int32, device
+ *   strides     host array of 6 element strides, {batch, head} of q, k and v; NULL
+ *               means dense.
+ *   slots >= sinks + window; the rest as for gdn2_swa_fwd.
+ */
+gdn2_status gdn2_swa_decode(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                            const int *pos, void *o, int B, int slots, int Hq, int Hk, int d, int window, int sinks,
+                            float scale, const long long *strides, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_scan_fwd -- the gated linear recurrence: the state update of the gated
+ * delta rule without its erase, one value per channel,
+ *     h_t = alpha_t h_{t-1} + w_t x_t,   alpha_t = exp(log_alpha_t),   y_t = h_t.
+ *
+ *   x, w        [B][T][C]  dtype   input and write gate
+ *   log_alpha   [B][T][C]  fp32    log of the decay (<= 0; -infinity forgets everything
+ *               before that token)
+ *   h0          [B][C]     fp32    initial state; NULL means zero
+ *   y           [B][T][C]  dtype   written
+ *   h_T         [B][C]     fp32    final state; NULL means not written.  May alias h0.
+ *   ckpt        [B][ceil(T / GDN2_SCAN_BLOCK)][C]  fp32  the state entering every
+ *               block of GDN2_SCAN_BLOCK tokens, for gdn2_scan_bwd; NULL means not
+ *               written.
+ *   B, C >= 1; T >= 0 (T = 0 only copies h0, or zeros, into h_T).
+ *
+ * The state is fp32 throughout.
+ */
+#define GDN2_SCAN_BLOCK 16
+gdn2_status gdn2_scan_fwd(const void *x, const void *w, const float *log_alpha, const float *h0, void *y,
+                          float *h_T, float *ckpt, int B, int T, int C, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_scan_bwd -- gradients of sum(y * dy) + sum(h_T * dh_T): with
+ * g_t = dy_t + alpha_{t+1} g_{t+1} (and dh_T added at the last token),
+ *     dx_t = w_t g_t,   dw_t = x_t g_t,   dlog_alpha_t = g_t alpha_t h_{t-1},
+ *     dh0 = alpha_1 g_1.
+ *
+ *   x, w, log_alpha, B, T, C, dtype   as for gdn2_scan_fwd
+ *   ckpt        written by gdn2_scan_fwd on the same inputs; h_{t-1} is recomputed
+ *               from it in fp32
+ *   dy          [B][T][C]  dtype   incoming gradient of y
+ *   dh_T        [B][C]     fp32    incoming gradient of h_T; NULL means zero
+ *   dx, dw      [B][T][C]  dtype   written
+ *   dlog_alpha  [B][T][C]  fp32    written
+ *   dh0         [B][C]     fp32    written; NULL means not wanted
+ */
+gdn2_status gdn2_scan_bwd(const void *x, const void *w, const float *log_alpha, const float *ckpt, const void *dy,
+                          const float *dh_T, void *dx, void *dw, float *dlog_alpha, float *dh0,
+                          int B, int T, int C, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_scan_step -- one token of the recurrence, the state updated in place.
+ *   x, w, y [B][C] dtype; log_alpha, h [B][C] fp32; y and h written.
+ */
+gdn2_status gdn2_scan_step(const void *x, const void *w, const float *log_alpha, float *h, void *y,
+                           int B, int C, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_block_norm_fwd -- the norms around a block, fused with the block's gate and
+ * residual scale: the block's output y is normalised, gated and added to the
+ * residual stream r, and the sum is normalised for the next block.  Per row:
+ *     r_out = r + res_scale (*) sigmoid(g_logit) (*) (y / rms(y)) (*) w_post
+ *     x_out = (r_out / rms(r_out)) (*) w_pre          rms(a) = sqrt(mean(a^2) + eps)
+ * x_out is formed from r_out before its rounding.
+ *
+ *   r, y        [N][D]  dtype   residual stream, block output
+ *   g_logit     [N][D]  dtype   gate logits; NULL means no gate (sigmoid -> 1)
+ *   w_post, res_scale, w_pre  [D]  fp32
+ *   eps         >= 0, finite
+ *   r_out, x_out  [N][D]  dtype  written; r_out may alias r
+ *   N >= 0; 1 <= D <= 16384.
+ */
+gdn2_status gdn2_block_norm_fwd(const void *r, const void *y, const void *g_logit, const float *w_post,
+                                const float *res_scale, const float *w_pre, float eps, void *r_out, void *x_out,
+                                long long N, int D, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_block_norm_bwd -- gradients of sum(r_out * dr_out) + sum(x_out * dx_out).  The
+ * forward's inputs are read again and its rows recomputed (as many bytes as reading
+ * r_out instead, and no rounding between).
+ *
+ *   r .. eps, N, D, dtype   as for gdn2_block_norm_fwd
+ *   dr_out, dx_out          [N][D]  dtype  incoming gradients
+ *   dr, dy, dg_logit        [N][D]  dtype  written; dr may alias dr_out; dg_logit is NULL
+ *                           exactly when g_logit is
+ *   dw_post, dres_scale, dw_pre  [D]  fp32  written: sums over the rows, in a fixed order
+ *                           (no atomics: repeated calls give identical bits)
+ * Takes its workspace (partial sums) from the library's pool.
+ */
+gdn2_status gdn2_block_norm_bwd(const void *r, const void *y, const void *g_logit, const float *w_post,
+                                const float *res_scale, const float *w_pre, float eps, const void *dr_out,
+                                const void *dx_out, void *dr, void *dy, void *dg_logit, float *dw_post,
+                                float *dres_scale, float *dw_pre, long long N, int D, gdn2_dtype dtype,
+                                gdn2_stream_t stream);
+
+/*
  * gdn2_check_device_error -- wait for `stream`, then read and clear the
  * device error word of the current device.  Returns GDN2_OK,
  * GDN2_ERR_DEVICE_TIMEOUT or GDN2_ERR_CUDA.
