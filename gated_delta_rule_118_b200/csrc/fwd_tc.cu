@@ -35,18 +35,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// 4-D map over a [B][T][H][d] tensor: dims (d, H, T, B), box (box_d, 1, 64, 1).
-bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, int d, int H, int T, int B,
-              int box_d, CUtensorMapSwizzle swz)
+// 4-D map over a tensor of axes (B, T, H, d) with rows of d contiguous elements and
+// the given element strides of the others: dims (d, H, T, B), box (box_d, 1, box_t, 1).
+bool make_strided_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, int d, int H, int T, int B,
+                      const long long (&st)[3], int box_d, int box_t, CUtensorMapSwizzle swz)
 {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)d * esize, (cuuint64_t)H * d * esize, (cuuint64_t)T * H * d * esize};
-    cuuint32_t box[4] = {(cuuint32_t)box_d, 1, 64, 1};
+    cuuint64_t strides[3] = {(cuuint64_t)st[2] * esize, (cuuint64_t)st[1] * esize, (cuuint64_t)st[0] * esize};
+    cuuint32_t box[4] = {(cuuint32_t)box_d, 1, (cuuint32_t)box_t, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(m, dt, 4, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same over a dense [B][T][H][d] tensor, boxes of 64 tokens.
+bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, int d, int H, int T, int B,
+              int box_d, CUtensorMapSwizzle swz)
+{
+    const long long st[3] = {(long long)T * H * d, (long long)H * d, d};
+    return make_strided_map(m, base, dt, esize, d, H, T, B, st, box_d, 64, swz);
 }
 
 // Stream-ordered pool for the workspace; it keeps freed blocks for reuse.
@@ -75,6 +84,12 @@ cudaMemPool_t workspace_pool(int dev)
 bool make_token_map(CUtensorMap *m, const void *base, int d, int H, int T, int B)
 {
     return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, H, T, B, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_rows_map(CUtensorMap *m, const void *base, int d, int H, int T, int B, const long long (&st)[3], int box_t)
+{
+    return make_strided_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, H, T, B, st, 64, box_t,
+                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor maps of the TMA-loaded inputs: q, k, b, log_alpha and the output-gate

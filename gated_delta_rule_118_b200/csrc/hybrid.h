@@ -23,7 +23,8 @@ struct SwaArgs {
     float scale;
     unsigned int *err;               // device error word
 };
-cudaError_t launch_swa_fwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t stream);     // fp32
+cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t stream);  // bf16
 cudaError_t launch_swa_bwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_swa_delta(const SwaArgs &a, bool bf16, cudaStream_t stream);
 

@@ -100,7 +100,8 @@ extern "C" gdn2_status gdn2_swa_fwd(const void *q, const void *k, const void *v,
     a.lse = lse;
     int sms = 0;
     if (!device_info(&a.err, &sms)) return GDN2_ERR_CUDA;
-    return from_cuda(launch_swa_fwd_simt(a, dtype == GDN2_BF16, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(dtype == GDN2_BF16 ? launch_swa_fwd_tc(a, s) : launch_swa_fwd_simt(a, s));
 }
 
 extern "C" gdn2_status gdn2_swa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,

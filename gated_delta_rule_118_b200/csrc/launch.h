@@ -108,6 +108,8 @@ cudaError_t run_fwd_tc(const FwdArgs &a, const FwdTcPlan &p, uint8_t *ws);
 // tokens with the 128-byte swizzle.
 bool make_input_maps(const FwdArgs &a, CUtensorMap *maps);
 bool make_token_map(CUtensorMap *m, const void *base, int d, int H, int T, int B);
+// The same with element strides {batch, token, head} and boxes of box_t tokens.
+bool make_rows_map(CUtensorMap *m, const void *base, int d, int H, int T, int B, const long long (&st)[3], int box_t);
 cudaError_t launch_fwd_tc(const FwdArgs &a);
 // `overlap`: launch as a programmatic dependent of the previous kernel in the
 // stream, so that it may start before that kernel ends (only where the two

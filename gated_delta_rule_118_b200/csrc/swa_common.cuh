@@ -21,7 +21,7 @@
 namespace gdn2 {
 namespace swa {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int seq_len(const SwaArgs &a, int b)
@@ -115,7 +115,7 @@ __device__ __noinline__ void row_forward(const SwaArgs &a, int b, int h, int i)
     for (int c = 0; c < n; c += 32) {
         const int t = c + lane, j = t < ns ? t : lo + t - ns;
         const bool on = t < n;
-        const float s = on ? dot_rows<E, D>(q, k[j]) * (a.scale * kLog2e) : -INFINITY;
+        const float s = on ? dot_rows<E, D>(q, k[j]) * (a.scale * kLog2E) : -INFINITY;
         const float mn = fmaxf(m, warp_max(s)), ms = mn == -INFINITY ? 0.f : mn;
         const float f = exp2f(m - ms), e = on ? exp2f(s - ms) : 0.f;
         m = mn;
@@ -141,7 +141,7 @@ __device__ __noinline__ void row_forward(const SwaArgs &a, int b, int h, int i)
 // exp(scale * s - lse) of a visible pair; 0 for a row without any finite score.
 __device__ __forceinline__ float prob(float s, float scale_log2e, float lse)
 {
-    return lse == -INFINITY ? 0.f : exp2f(s * scale_log2e - lse * kLog2e);
+    return lse == -INFINITY ? 0.f : exp2f(s * scale_log2e - lse * kLog2E);
 }
 
 // Row i of dq, by one warp.
@@ -162,7 +162,7 @@ __device__ __noinline__ void row_dq(const SwaArgs &a, int b, int h, int i)
         const int t = c + lane, j = t < ns ? t : lo + t - ns;
         float ds = 0.f;
         if (t < n)
-            ds = prob(dot_rows<E, D>(q, k[j]), a.scale * kLog2e, lse) * (dot_rows<E, D>(g, v[j]) - delta) * a.scale;
+            ds = prob(dot_rows<E, D>(q, k[j]), a.scale * kLog2E, lse) * (dot_rows<E, D>(g, v[j]) - delta) * a.scale;
         const int live = n - c < 32 ? n - c : 32;
         for (int r = 0; r < live; ++r) {
             const int tr = c + r, jr = tr < ns ? tr : lo + tr - ns;
@@ -194,7 +194,7 @@ __device__ __noinline__ void row_dkdv(const SwaArgs &a, int b, int hk, int j)
             const int i = c + lane;
             float pr = 0.f, ds = 0.f;
             if (i < i1) {
-                pr = prob(dot_rows<E, D>(q[i], k), a.scale * kLog2e, a.lse[row + i]);
+                pr = prob(dot_rows<E, D>(q[i], k), a.scale * kLog2E, a.lse[row + i]);
                 ds = pr * (dot_rows<E, D>(g[i], v) - a.delta[row + i]) * a.scale;
             }
             const int live = i1 - c < 32 ? i1 - c : 32;

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs
     for (int g = 0; g < GC; ++g) {
         const E *qr = static_cast<const E *>(a.q) + b * a.qs[0] + (long long)(hk * G + g0 + min(g, ng - 1)) * a.qs[1];
         const float4 f = load4(qr + x);
-        const float sc = a.scale * kLog2e;
+        const float sc = a.scale * kLog2E;
         q[g][0] = f.x * sc; q[g][1] = f.y * sc; q[g][2] = f.z * sc; q[g][3] = f.w * sc;
         m[g] = -INFINITY;
         l[g] = o[g][0] = o[g][1] = o[g][2] = o[g][3] = 0.f;

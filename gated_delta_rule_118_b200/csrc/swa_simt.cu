@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = sees(p0 + ty * 4 + i, j0 + tx + 16 * j, a.window, a.sinks) ? s[i][j] * (a.scale * kLog2e)
+                    s[i][j] = sees(p0 + ty * 4 + i, j0 + tx + 16 * j, a.window, a.sinks) ? s[i][j] * (a.scale * kLog2E)
                                                                                         : -INFINITY;
                     mx = fmaxf(mx, s[i][j]);
                 }
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
                 for (int j = 0; j < 2; ++j) {
                     const bool on = sees(p0 + ty * 4 + i, j0 + tx + 16 * j, a.window, a.sinks);
                     Ps[(ty * 4 + i) * PS + tx + 16 * j] =
-                        on ? prob(s[i][j], a.scale * kLog2e, lse[i]) * (dp[i][j] - delta[i]) : 0.f;
+                        on ? prob(s[i][j], a.scale * kLog2E, lse[i]) * (dp[i][j] - delta[i]) : 0.f;
                 }
             __syncthreads();
             mul_tile<D, 32, PS>(acc, Ps, ty * 4, Ks, tx);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool on = t < n && sees(off + t, j0 + tx + 16 * j, a.window, a.sinks);
-                    s[i][j] = on ? prob(s[i][j], a.scale * kLog2e, lse) : 0.f;
+                    s[i][j] = on ? prob(s[i][j], a.scale * kLog2E, lse) : 0.f;
                     dp[i][j] = on ? s[i][j] * (dp[i][j] - delta) : 0.f;
                     Ps[(ty * 2 + i) * PS + tx + 16 * j] = s[i][j];
                 }
@@ -379,9 +379,8 @@ cudaError_t delta_impl(const SwaArgs &a, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_swa_fwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream)
+cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t stream)
 {
-    if (bf16) return a.d == 128 ? fwd_impl<__nv_bfloat16, 128>(a, stream) : fwd_impl<__nv_bfloat16, 64>(a, stream);
     return a.d == 128 ? fwd_impl<float, 128>(a, stream) : fwd_impl<float, 64>(a, stream);
 }
 
