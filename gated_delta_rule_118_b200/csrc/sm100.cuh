@@ -17,6 +17,18 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
 {
@@ -178,6 +190,13 @@ __device__ __forceinline__ uint64_t global_ns()
     return t;
 }
 
+// Register split between the warpgroups of a CTA (every warp of the warpgroup
+// executes it; the shares add up to at most the launch's registers).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // Let the next kernel of the stream, if it was launched as a programmatic
 // dependent, start while this grid is still running (a no-op otherwise).
@@ -186,6 +205,33 @@ __device__ __forceinline__ void allow_dependent_launch() { asm volatile("griddep
 // Wait until the grid this one was launched as a programmatic dependent of has
 // completed and its memory operations are visible (returns at once otherwise).
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------- cluster launch control
+// Ask for a CTA of this grid that has not started yet, to run its work here instead:
+// 16 bytes arrive in `response` and complete on `bar` (after mbar_arrive_expect_tx of
+// 16).  After one request came back empty no other may be made.
+__device__ __forceinline__ void next_cta_request(void *response, uint64_t *bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(response)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The answer: true and the CTA's index, or false when none was left.
+__device__ __forceinline__ bool next_cta(const void *response, int &x, int &y, int &z)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %3, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}"
+        : "+r"(x), "+r"(y), "+r"(z), "=r"(ok)
+        : "r"(smem_u32(response))
+        : "memory");
+    return ok != 0;
+}
 
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols)
@@ -294,6 +340,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *u)
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Ties registers to this point of the program: a use of loaded values cannot be
+// scheduled above the wait that precedes it.
+template <int N>
+__device__ __forceinline__ void pin(float (&r)[N])
+{
+    static_assert(N % 16 == 0, "sixteen at a time");
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile(""
+                     : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
+                       "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]), "+f"(r[i + 10]), "+f"(r[i + 11]),
+                       "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]), "+f"(r[i + 15]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float (&r)[N])
+{
+    tmem_ld_wait();
+    pin(r);
+}
 
 // ---------------------------------------------------------------- UMMA descriptors
 // Swizzle modes of the shared-memory matrix descriptor (bits 61..63).

@@ -103,7 +103,7 @@ __device__ __forceinline__ Rows<E> dense_rows(const void *base, int b, int h, in
 
 // Row i of the forward, by one warp: o and lse written.
 template <typename E, int D>
-__device__ __noinline__ void row_forward(const SwaArgs &a, int b, int h, int i)
+__device__ __forceinline__ void row_forward(const SwaArgs &a, int b, int h, int i)
 {
     const int lane = threadIdx.x & 31, p = a.Tk - a.T + i;
     const E *q = rows_of<E>(a.q, a.qs, b, h)[i];
@@ -146,7 +146,7 @@ __device__ __forceinline__ float prob(float s, float scale_log2e, float lse)
 
 // Row i of dq, by one warp.
 template <typename E, int D>
-__device__ __noinline__ void row_dq(const SwaArgs &a, int b, int h, int i)
+__device__ __forceinline__ void row_dq(const SwaArgs &a, int b, int h, int i)
 {
     const int lane = threadIdx.x & 31, p = a.Tk - a.T + i;
     const E *q = rows_of<E>(a.q, a.qs, b, h)[i];
@@ -178,7 +178,7 @@ __device__ __noinline__ void row_dq(const SwaArgs &a, int b, int h, int i)
 
 // Row j of dk and dv, by one warp.
 template <typename E, int D>
-__device__ __noinline__ void row_dkdv(const SwaArgs &a, int b, int hk, int j)
+__device__ __forceinline__ void row_dkdv(const SwaArgs &a, int b, int hk, int j)
 {
     const int lane = threadIdx.x & 31, off = a.Tk - a.T, G = a.Hq / a.Hk;
     const E *k = rows_of<E>(a.k, a.ks, b, hk)[j], *v = rows_of<E>(a.v, a.vs, b, hk)[j];
