@@ -1,0 +1,649 @@
+// swa_bwd_tc.cu -- windowed attention backward for bf16 on the tensor cores.
+//
+// Two kernels, so that every sum has one owner and a fixed order (no atomics): dk and dv
+// by key tiles, dq by query tiles.  Scores and dO v^T are formed in both (7 products of
+// 128 x 128 x d a tile pair instead of 5).  In both kernels the matrix that a product
+// reads as its left operand (P^T, dS^T, or dS) is written as bf16 straight into tensor
+// memory over the fp32 values it came from, so nothing but the inputs passes through
+// shared memory:
+//   dk, dv:  S^T = K Q^T,  dP^T = V dO^T     one key row per thread pair (64 queries each)
+//            P^T = exp(scale S^T - lse),  dS^T = P^T (dP^T - delta)
+//            dV += P^T dO,  dK += dS^T Q
+//   dq:      S = Q K^T,  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K
+// P and dS are rounded to bf16 (2^-8 relative at most, as operands of bf16 products);
+// scores, probabilities' exponents, sums and gradients are fp32 up to the one rounding
+// on the way out.
+//
+// Keys that every later row sees (sinks) have as many query tiles as the sequence;
+// where that would leave a few CTAs with most of the work, their query range is split
+// into segments whose fp32 partial sums a small kernel adds in order.
+#include <cuda.h>
+
+#include "launch.h"
+#include "sm100.cuh"
+#include "swa_common.cuh"
+#include "tc_common.cuh"
+
+namespace gdn2 {
+namespace {
+
+using namespace swa;
+using namespace sm100;
+
+constexpr int kThreads = 384;  // two warpgroups that compute, then the issuing warps
+constexpr int kTma = 8, kMma = 9, kRows = 10;
+// 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 = 384 x 168
+constexpr int kRegsCompute = 216, kRegsIssue = 72;
+
+template <int D>
+struct Tiles {
+    static constexpr int TILE = 128 * D * 2;  // bytes of a 128-row tile, boxes of 64 channels
+    static constexpr uint32_t STEP = TILE >> 4;
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int h, int row, int b)
+{
+    for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * 16384, m, bar, x * 64, h, row, b);
+}
+
+// D[128 x 128] = A B^T over d: both tiles in shared memory, rows of d.
+template <int D>
+__device__ __forceinline__ void issue_rows(uint32_t tm, uint64_t da, uint64_t db)
+{
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t o = (ks >> 2) * 1024 + (ks & 3) * 2;
+        umma_bf16(tm, da + o, db + o, idesc_bf16(128, 128, 0, 0), ks > 0);
+    }
+}
+// D[128 x d] += A B: A bf16 in tensor memory (128 columns, 64 of them from tm_a, 64 from
+// tm_a + 64), B a tile of 128 rows of d.
+template <int D>
+__device__ __forceinline__ void issue_cols(uint32_t tm, uint32_t tm_a, uint64_t db, uint32_t acc)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        umma_bf16_ts(tm, tm_a + (ks >> 2) * 64 + (ks & 3) * 8, db + ks * 128, idesc_bf16(128, D, 0, 1), acc | (ks > 0));
+}
+
+// 64 values packed to bf16 over the columns they came from.
+__device__ __forceinline__ void put_bf16(uint32_t tm, const float (&f)[64])
+{
+    uint32_t u[32];
+#pragma unroll
+    for (int x = 0; x < 64; x += 2) {
+        const __nv_bfloat162 e = __floats2bfloat162_rn(f[x], f[x + 1]);
+        u[x / 2] = *reinterpret_cast<const uint32_t *>(&e);
+    }
+    tmem_st32(tm, u);
+    tmem_st_wait();
+    tc_fence_before();
+}
+
+// Half a row (D / 2 columns from tm) scaled and written, or zeros where not `live`; true
+// if something is not finite.  `have` (the same in the whole warp): there are values in tm.
+template <int D, typename E>
+__device__ __forceinline__ bool put_row(uint32_t tm, float f, E *dst, bool inside, bool live, bool have)
+{
+    bool bad = false;
+#pragma unroll
+    for (int x = 0; x < D / 2; x += 32) {
+        float o[32];
+        if (have) {
+            tmem_ld32(tm + x, o);
+            tmem_ld_wait(o);
+        }
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+            o[y] = have && live ? o[y] * f : 0.f;
+            bad |= !isfinite(o[y]);
+        }
+        if (inside)
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) store4(dst + x + y, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
+    }
+    return bad && inside;
+}
+
+// ---------------------------------------------------------------- dk, dv
+// The work of one CTA along grid x: a key tile and its range of query tiles.
+struct KvPlan {
+    int nseg;      // segments of a sink tile's queries; 0: no splitting
+    int seg;       // query tiles of a segment
+    int nsink;     // key tiles with sinks
+    int ntiles;    // key tiles
+    float *part;   // [B][Hk][nsink][nseg][2][128][d] partial sums
+};
+
+struct KvRange {
+    int j0, q0, q1, slot;  // first key, query tiles [q0, q1), partial slot (-1: final)
+    __device__ __forceinline__ KvRange(const SwaArgs &a, const KvPlan &p, int x, int n)
+    {
+        const int off = a.Tk - a.T, split = p.nseg ? p.nsink * p.nseg : 0;
+        slot = x < split ? x : -1;
+        const int tile = x < split ? x / p.nseg : x - split + (p.nseg ? p.nsink : 0);
+        j0 = tile * 128;
+        q0 = (j0 > off ? j0 - off : 0) >> 7;
+        const long long far = (long long)min(j0 + 128, a.Tk) - 1 + a.window - off;  // first row behind every window
+        const int hi = (j0 < a.sinks || far > n) ? n : far < 0 ? 0 : (int)far;
+        q1 = (hi + 127) >> 7;
+        if (slot >= 0) {
+            q0 += x % p.nseg * p.seg;
+            q1 = min(q1, q0 + p.seg);
+        }
+    }
+};
+
+enum { KV_FULL, QG_FULL, QG_EMPTY = QG_FULL + 2, LD_FULL = QG_EMPTY + 2, LD_EMPTY = LD_FULL + 2,
+       S_FULL = LD_EMPTY + 2, DP_FULL, P_FULL, DS_FULL, DONE, NBAR };
+
+template <int D>
+struct KvLayout {
+    static constexpr int TILE = Tiles<D>::TILE;
+    static constexpr int K = 0, V = TILE, Q = 2 * TILE, G = 4 * TILE;
+    static constexpr int LD = 6 * TILE;            // [stage][lse, delta][128] fp32
+    static constexpr int BAR = LD + 2048;
+    static constexpr int SLOT = BAR + 8 * NBAR + 8;
+    static constexpr int BYTES = SLOT + 16 + 1024;
+    static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __grid_constant__ CUtensorMap mq,
+               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+               const __grid_constant__ CUtensorMap mg)
+{
+    using L = KvLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = blockIdx.y, b = blockIdx.z;
+    const int n = seq_len(a, b), off = a.Tk - a.T, G = a.Hq / a.Hk;
+    const KvRange rg(a, plan, blockIdx.x, n);
+    const int nq = max(rg.q1 - rg.q0, 0), N = G * nq;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
+    float *ld = reinterpret_cast<float *>(sm + L::LD);
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) mbar_init(bar + i, i == P_FULL || i == DS_FULL || i == LD_EMPTY || i == LD_EMPTY + 1 ? 8 : 1);
+        fence_mbar_init();
+    }
+    if (warp == kMma) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const uint32_t sbase = smem_u32(sm);
+    auto head = [&](int i) { return hk * G + i / nq; };
+    auto row0 = [&](int i) { return (rg.q0 + i % nq) * 128; };
+
+    if (warp >= 8) {
+        setmaxnreg_dec<kRegsIssue>();
+        if (warp == kTma && N > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar + KV_FULL, 2 * L::TILE);
+                load_tile<D>(sm + L::K, &mk, bar + KV_FULL, hk, rg.j0, b);
+                load_tile<D>(sm + L::V, &mv, bar + KV_FULL, hk, rg.j0, b);
+            }
+            __syncwarp();
+            int i = 0;
+            for (; i < N; ++i) {
+                const int s = i & 1;
+                if (!__all_sync(~0u, mbar_wait(bar + QG_EMPTY + s, ((i >> 1) & 1) ^ 1, a.err))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar + QG_FULL + s, 2 * L::TILE);
+                    load_tile<D>(sm + L::Q + s * L::TILE, &mq, bar + QG_FULL + s, head(i), row0(i), b);
+                    load_tile<D>(sm + L::G + s * L::TILE, &mg, bar + QG_FULL + s, head(i), row0(i), b);
+                }
+                __syncwarp();
+            }
+            // every copy has landed before the CTA ends, also when another role gave up
+            mbar_wait(bar + KV_FULL, 0, a.err);
+            for (int c = max(i - 2, 0); c < i; ++c) mbar_wait(bar + QG_FULL + (c & 1), (c >> 1) & 1, a.err);
+        } else if (warp == kRows) {
+            // lse (in log2, +infinity for rows without a token or without a finite score, so
+            // that their probabilities come out 0) and delta of the tile's rows
+            for (int i = 0; i < N; ++i) {
+                const int s = i & 1;
+                if (!__all_sync(~0u, mbar_wait(bar + LD_EMPTY + s, ((i >> 1) & 1) ^ 1, a.err))) break;
+                const long long at = ((long long)b * a.Hq + head(i)) * a.T;
+#pragma unroll
+                for (int x = lane; x < 128; x += 32) {
+                    const int row = row0(i) + x;
+                    const float l = row < n ? a.lse[at + row] : -INFINITY;
+                    ld[s * 256 + x] = l == -INFINITY ? INFINITY : l * kLog2E;
+                    ld[s * 256 + 128 + x] = row < n ? a.delta[at + row] : 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + LD_FULL + s);
+            }
+        } else if (warp == kMma && N > 0) {
+            const uint64_t dk = smem_desc(sbase + L::K, 16, 1024, kSw128), dv = smem_desc(sbase + L::V, 16, 1024, kSw128);
+            const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dg = smem_desc(sbase + L::G, 16, 1024, kSw128);
+            const uint64_t qt = smem_desc(sbase + L::Q, 16384, 1024, kSw128), gt = smem_desc(sbase + L::G, 16384, 1024, kSw128);
+            constexpr uint32_t STEP = Tiles<D>::STEP;
+            bool ok = mbar_wait(bar + KV_FULL, 0, a.err) && mbar_wait(bar + QG_FULL, 0, a.err);
+            ok = __all_sync(~0u, ok);
+            if (ok) {
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_rows<D>(tmem + L::TM_S, dk, dq);
+                    umma_commit(bar + S_FULL);
+                    issue_rows<D>(tmem + L::TM_DP, dv, dg);
+                    umma_commit(bar + DP_FULL);
+                }
+                __syncwarp();
+            }
+            for (int i = 0; ok && i < N; ++i) {
+                const uint32_t s = i & 1, sn = s ^ 1;
+                const bool next = i + 1 < N;
+                ok = mbar_wait(bar + P_FULL, s, a.err);
+                if (ok && next) ok = mbar_wait(bar + QG_FULL + sn, ((i + 1) >> 1) & 1, a.err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_cols<D>(tmem + L::TM_DV, tmem + L::TM_S, gt + s * STEP, i > 0);
+                    if (next) {  // over P^T, which the product just issued reads: products run in order
+                        issue_rows<D>(tmem + L::TM_S, dk, dq + sn * STEP);
+                        umma_commit(bar + S_FULL);
+                    }
+                }
+                __syncwarp();
+                ok = __all_sync(~0u, mbar_wait(bar + DS_FULL, s, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_cols<D>(tmem + L::TM_DK, tmem + L::TM_DP, qt + s * STEP, i > 0);
+                    umma_commit(bar + QG_EMPTY + s);
+                    if (next) {
+                        issue_rows<D>(tmem + L::TM_DP, dv, dg + sn * STEP);
+                        umma_commit(bar + DP_FULL);
+                    }
+                }
+                __syncwarp();
+            }
+            if (elect_one()) umma_commit(bar + DONE);
+            __syncwarp();
+            mbar_wait(bar + DONE, 0, a.err);  // no product is in flight when the tensor memory is freed
+        }
+    } else {
+        setmaxnreg_inc<kRegsCompute>();
+        const int hf = warp >> 2, r = tid & 127, j = rg.j0 + r;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + L::TM_S + hf * 64, tp = lane_base + L::TM_DP + hf * 64;
+        const float sc = a.scale * kLog2E;
+        bool ok = true;
+        for (int i = 0; i < N; ++i) {
+            const int s = i & 1, i0 = row0(i), c0 = i0 + hf * 64;
+            const float *lse2 = ld + s * 256 + hf * 64, *delta = lse2 + 128;
+            ok = mbar_wait(bar + LD_FULL + s, (i >> 1) & 1, a.err) && mbar_wait(bar + S_FULL, s, a.err);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after();
+            float p[64];
+            tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(p));
+            tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+            tmem_ld_wait(p);
+            // (rows behind the length have p = 0 by their lse, but what stands in their dO
+            // must not reach the product with it)
+            const bool full = i0 + 128 <= n && tile_full(off + i0, off + i0 + 127, rg.j0, rg.j0 + 128, a.window, a.sinks);
+            if (!full) {
+                const int lo = j - off - c0;
+                const long long far = (long long)lo + a.window;
+                const int hi = j < a.sinks || far > n - c0 ? n - c0 : (int)far;
+#pragma unroll
+                for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : -INFINITY;
+            }
+#pragma unroll
+            for (int x = 0; x < 64; x += 4) {
+                const float4 e = *reinterpret_cast<const float4 *>(lse2 + x);
+                p[x] = ex2_approx(fmaf(p[x], sc, -e.x));
+                p[x + 1] = ex2_approx(fmaf(p[x + 1], sc, -e.y));
+                p[x + 2] = ex2_approx(fmaf(p[x + 2], sc, -e.z));
+                p[x + 3] = ex2_approx(fmaf(p[x + 3], sc, -e.w));
+            }
+            put_bf16(ts, p);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + P_FULL);
+            ok = __all_sync(~0u, mbar_wait(bar + DP_FULL, s, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            float g[64];
+            tmem_ld32(tp, *reinterpret_cast<float(*)[32]>(g));
+            tmem_ld32(tp + 32, *reinterpret_cast<float(*)[32]>(g + 32));
+            tmem_ld_wait(g);
+#pragma unroll
+            for (int x = 0; x < 64; x += 4) {
+                const float4 e = *reinterpret_cast<const float4 *>(delta + x);
+                g[x] = p[x] * (g[x] - e.x);
+                g[x + 1] = p[x + 1] * (g[x + 1] - e.y);
+                g[x + 2] = p[x + 2] * (g[x + 2] - e.z);
+                g[x + 3] = p[x + 3] * (g[x + 3] - e.w);
+            }
+            if (!full)
+#pragma unroll
+                for (int x = 0; x < 64; ++x) g[x] = p[x] == 0.f ? 0.f : g[x];
+            put_bf16(tp, g);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar + DS_FULL);
+                mbar_arrive(bar + LD_EMPTY + s);
+            }
+        }
+        if (ok && N > 0) ok = mbar_wait(bar + DONE, 0, a.err);
+        ok = named_bar_and(1, 256, ok);
+        tc_fence_after();
+        if (ok) {
+            const uint32_t tv = lane_base + L::TM_DV + hf * (D / 2), tk = lane_base + L::TM_DK + hf * (D / 2);
+            const bool have = N > 0, inside = j < a.Tk;
+            if (rg.slot >= 0) {  // partial sums of a segment
+                float *part = plan.part + ((((long long)b * a.Hk + hk) * plan.nsink * plan.nseg + rg.slot) * 256 + r) * D + hf * (D / 2);
+                put_row<D>(tk, a.scale, part, true, true, have);
+                put_row<D>(tv, 1.f, part + 128 * D, true, true, have);
+            } else {
+                const long long at = (((long long)b * a.Tk + j) * a.Hk + hk) * D + hf * (D / 2);
+                bool bad = put_row<D>(tk, a.scale, static_cast<bf16 *>(a.dk) + at, inside, true, have);
+                bad |= put_row<D>(tv, 1.f, static_cast<bf16 *>(a.dv) + at, inside, true, have);
+                uint32_t *bads = reinterpret_cast<uint32_t *>(ld);  // (no more rows of lse are read)
+                bads[hf * 128 + r] = bad;
+                named_bar(1, 256);
+                unsigned todo = __ballot_sync(~0u, hf == 0 && (bads[r] | bads[128 + r]));
+                while (todo) {
+                    const int r0 = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    row_dkdv<bf16, D>(a, b, hk, j - lane + r0);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dk and dv of the sink tiles: the segments' partial sums added in order, one warp a key.
+template <int D>
+__global__ void __launch_bounds__(256) sink_sum_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan)
+{
+    const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, hk = blockIdx.y, b = blockIdx.z;
+    if (j >= plan.nsink * 128 || j >= a.Tk) return;
+    const float *part = plan.part + ((((long long)b * a.Hk + hk) * plan.nsink + (j >> 7)) * plan.nseg * 256 + (j & 127)) * D;
+    bool bad = false;
+    float v[2][D / 32] = {};
+    for (int s = 0; s < plan.nseg; ++s)
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) v[w][u] += part[((long long)s * 256 + w * 128) * D + lane + 32 * u];
+    const long long at = (((long long)b * a.Tk + j) * a.Hk + hk) * D;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        bad |= !isfinite(v[0][u]) || !isfinite(v[1][u]);
+        static_cast<bf16 *>(a.dk)[at + lane + 32 * u] = __float2bfloat16_rn(v[0][u]);
+        static_cast<bf16 *>(a.dv)[at + lane + 32 * u] = __float2bfloat16_rn(v[1][u]);
+    }
+    if (__any_sync(~0u, bad)) row_dkdv<bf16, D>(a, b, hk, j);
+}
+
+// ---------------------------------------------------------------- dq
+enum { QD_FULL, K_FULL, K_EMPTY = K_FULL + 2, V_FULL = K_EMPTY + 2, V_EMPTY = V_FULL + 2, SQ_FULL = V_EMPTY + 2, SQ_FREE,
+       DPQ_FULL, DSQ_FULL = DPQ_FULL + 2, DONE_Q = DSQ_FULL + 2, NBAR_Q };
+
+template <int D>
+struct QLayout {
+    static constexpr int TILE = Tiles<D>::TILE;
+    static constexpr int Q = 0, G = TILE, K = 2 * TILE, V = 4 * TILE;
+    static constexpr int BAD = 6 * TILE;           // [half][128]
+    static constexpr int BAR = BAD + 1024;
+    static constexpr int SLOT = BAR + 8 * NBAR_Q + 8;
+    static constexpr int BYTES = SLOT + 16 + 1024;
+    static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // two buffers of dP
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensorMap mq,
+             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+             const __grid_constant__ CUtensorMap mg)
+{
+    using L = QLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int i0 = (gridDim.x - 1 - blockIdx.x) * 128, h = blockIdx.y, b = blockIdx.z;  // longest rows first
+    const int n = seq_len(a, b), off = a.Tk - a.T, hk = h / (a.Hq / a.Hk);
+    if (i0 >= n) {  // padding only
+        const int rows = min(128, a.T - i0);
+        bf16 *out = static_cast<bf16 *>(a.dq) + (((long long)b * a.T + i0) * a.Hq + h) * D;
+        for (int c = tid; c < rows * (D / 8); c += kThreads)
+            *reinterpret_cast<uint4 *>(out + (long long)(c / (D / 8)) * a.Hq * D + c % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
+    if (tid == 0) {
+        for (int i = 0; i < NBAR_Q; ++i) mbar_init(bar + i, i == SQ_FREE || i == DSQ_FULL || i == DSQ_FULL + 1 ? 8 : 1);
+        fence_mbar_init();
+    }
+    if (warp == kMma) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const uint32_t sbase = smem_u32(sm);
+    const KeyTiles kt(off + i0, off + min(i0 + 128, n) - 1, a.window, a.sinks, 128);
+    const int N = kt.count();
+
+    if (warp >= 8) {
+        setmaxnreg_dec<kRegsIssue>();
+        if (warp == kTma) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar + QD_FULL, 2 * L::TILE);
+                load_tile<D>(sm + L::Q, &mq, bar + QD_FULL, h, i0, b);
+                load_tile<D>(sm + L::G, &mg, bar + QD_FULL, h, i0, b);
+            }
+            __syncwarp();
+            int nk = 0, nv = 0;
+            for (int c = 0; c < N; ++c) {
+                const int s = c & 1;
+                const uint32_t ph = ((c >> 1) & 1) ^ 1;
+                if (!__all_sync(~0u, mbar_wait(bar + K_EMPTY + s, ph, a.err))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar + K_FULL + s, L::TILE);
+                    load_tile<D>(sm + L::K + s * L::TILE, &mk, bar + K_FULL + s, hk, kt.tile(c) * 128, b);
+                }
+                __syncwarp();
+                nk = c + 1;
+                if (!__all_sync(~0u, mbar_wait(bar + V_EMPTY + s, ph, a.err))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar + V_FULL + s, L::TILE);
+                    load_tile<D>(sm + L::V + s * L::TILE, &mv, bar + V_FULL + s, hk, kt.tile(c) * 128, b);
+                }
+                __syncwarp();
+                nv = c + 1;
+            }
+            // every copy has landed before the CTA ends, also when another role gave up
+            mbar_wait(bar + QD_FULL, 0, a.err);
+            for (int c = max(nk - 2, 0); c < nk; ++c) mbar_wait(bar + K_FULL + (c & 1), (c >> 1) & 1, a.err);
+            for (int c = max(nv - 2, 0); c < nv; ++c) mbar_wait(bar + V_FULL + (c & 1), (c >> 1) & 1, a.err);
+        } else if (warp == kMma) {
+            const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dg = smem_desc(sbase + L::G, 16, 1024, kSw128);
+            const uint64_t dk = smem_desc(sbase + L::K, 16, 1024, kSw128), dv = smem_desc(sbase + L::V, 16, 1024, kSw128);
+            const uint64_t kt_ = smem_desc(sbase + L::K, 16384, 1024, kSw128);
+            constexpr uint32_t STEP = Tiles<D>::STEP;
+            bool ok = mbar_wait(bar + QD_FULL, 0, a.err);
+            // S and dP of tile c; S goes over the S that has been read, dP into the buffer whose
+            // dS was the operand of a product issued before
+            auto scores = [&](int c) {
+                const uint32_t s = c & 1, ph = (c >> 1) & 1;
+                ok = ok && mbar_wait(bar + K_FULL + s, ph, a.err) && mbar_wait(bar + V_FULL + s, ph, a.err);
+                if (c > 0) ok = ok && mbar_wait(bar + SQ_FREE, (c - 1) & 1, a.err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_rows<D>(tmem + L::TM_S, dq, dk + s * STEP);
+                    umma_commit(bar + SQ_FULL);
+                    issue_rows<D>(tmem + L::TM_DP + s * 128, dg, dv + s * STEP);
+                    umma_commit(bar + DPQ_FULL + s);
+                    umma_commit(bar + V_EMPTY + s);
+                }
+                __syncwarp();
+            };
+            scores(0);
+            for (int c = 0; ok && c < N; ++c) {
+                const uint32_t s = c & 1;
+                if (c + 1 < N) scores(c + 1);
+                ok = __all_sync(~0u, ok && mbar_wait(bar + DSQ_FULL + s, (c >> 1) & 1, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_cols<D>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + s * STEP, c > 0);
+                    umma_commit(bar + K_EMPTY + s);
+                }
+                __syncwarp();
+            }
+            if (elect_one()) umma_commit(bar + DONE_Q);
+            __syncwarp();
+            mbar_wait(bar + DONE_Q, 0, a.err);  // no product is in flight when the tensor memory is freed
+        }
+    } else {
+        setmaxnreg_inc<kRegsCompute>();
+        const int hf = warp >> 2, r = tid & 127, row = i0 + r, p_ = off + row;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sc = a.scale * kLog2E;
+        const long long lrow = ((long long)b * a.Hq + h) * a.T + row;
+        const bool live = row < n;
+        const float lse = live ? a.lse[lrow] : -INFINITY, delta = live ? a.delta[lrow] : 0.f;
+        const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2E;
+        bool ok = true;
+        for (int c = 0; c < N; ++c) {
+            const int s = c & 1, j0 = kt.tile(c) * 128, c0 = j0 + hf * 64;
+            const uint32_t tp = lane_base + L::TM_DP + s * 128 + hf * 64;
+            ok = __all_sync(~0u, mbar_wait(bar + SQ_FULL, s, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            float p[64];
+            tmem_ld32(lane_base + L::TM_S + hf * 64, *reinterpret_cast<float(*)[32]>(p));
+            tmem_ld32(lane_base + L::TM_S + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+            tmem_ld_wait(p);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + SQ_FREE);
+            const bool full = tile_full(off + i0, off + i0 + 127, j0, j0 + 128, a.window, a.sinks);
+            if (!full) {
+                const int hi = p_ - c0, lo = p_ - a.window + 1 - c0, sk = a.sinks - c0;
+#pragma unroll
+                for (int x = 0; x < 64; ++x) p[x] = x <= hi && (x >= lo || x < sk) ? p[x] : -INFINITY;
+            }
+#pragma unroll
+            for (int x = 0; x < 64; ++x) p[x] = ex2_approx(fmaf(p[x], sc, -lse2));
+            ok = __all_sync(~0u, mbar_wait(bar + DPQ_FULL + s, (c >> 1) & 1, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            float g[64];
+            tmem_ld32(tp, *reinterpret_cast<float(*)[32]>(g));
+            tmem_ld32(tp + 32, *reinterpret_cast<float(*)[32]>(g + 32));
+            tmem_ld_wait(g);
+#pragma unroll
+            for (int x = 0; x < 64; ++x) g[x] = p[x] * (g[x] - delta);
+            if (!full)
+#pragma unroll
+                for (int x = 0; x < 64; ++x) g[x] = p[x] == 0.f ? 0.f : g[x];
+            put_bf16(tp, g);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + DSQ_FULL + s);
+        }
+        if (ok) ok = mbar_wait(bar + DONE_Q, 0, a.err);
+        ok = named_bar_and(1, 256, ok);
+        tc_fence_after();
+        if (ok) {
+            const long long at = (((long long)b * a.T + row) * a.Hq + h) * D + hf * (D / 2);
+            const bool bad = put_row<D>(lane_base + L::TM_DQ + hf * (D / 2), a.scale, static_cast<bf16 *>(a.dq) + at,
+                                        row < a.T, live, true);
+            uint32_t *bads = reinterpret_cast<uint32_t *>(sm + L::BAD);
+            bads[hf * 128 + r] = bad;
+            named_bar(1, 256);
+            unsigned todo = __ballot_sync(~0u, hf == 0 && (bads[r] | bads[128 + r]));
+            while (todo) {
+                const int r0 = __ffs(todo) - 1;
+                todo &= todo - 1;
+                row_dq<bf16, D>(a, b, h, row - lane + r0);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// A sink tile's queries are split where the sink tiles alone are fewer CTAs than the
+// device has SMs twice over (with more of them they balance by themselves) and a
+// sequence has more query tiles than one segment.
+KvPlan plan_kv(const SwaArgs &a, int num_sms)
+{
+    KvPlan p{};
+    const int nqt = (a.T + 127) / 128;
+    p.ntiles = (a.Tk + 127) / 128;
+    p.nsink = (a.sinks + 127) / 128;
+    p.seg = nqt / 16 > 16 ? (nqt + 15) / 16 : 16;
+    p.nseg = (nqt + p.seg - 1) / p.seg;
+    if (p.nseg < 2 || (long long)a.B * a.Hk * p.nsink > 2LL * num_sms) p.nseg = 0;
+    return p;
+}
+
+template <int D>
+cudaError_t impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
+{
+    KvPlan plan = plan_kv(a, num_sms);
+    plan.part = part;
+    static std::atomic<unsigned long long> kv_set{0}, q_set{0};
+    cudaError_t e = ensure_smem_limit(dkdv_tc_kernel<D>, KvLayout<D>::BYTES, kv_set);
+    if (e == cudaSuccess) e = ensure_smem_limit(dq_tc_kernel<D>, QLayout<D>::BYTES, q_set);
+    if (e != cudaSuccess) return e;
+    const long long gs[3] = {(long long)a.T * a.Hq * D, (long long)a.Hq * D, D};
+    CUtensorMap mq, mk, mv, mg;
+    if (!make_rows_map(&mq, a.q, D, a.Hq, a.T, a.B, a.qs, 128) || !make_rows_map(&mk, a.k, D, a.Hk, a.Tk, a.B, a.ks, 128) ||
+        !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128) || !make_rows_map(&mg, a.dO, D, a.Hq, a.T, a.B, gs, 128))
+        return cudaErrorInvalidValue;
+    const int items = plan.nseg ? plan.nsink * plan.nseg + plan.ntiles - plan.nsink : plan.ntiles;
+    dkdv_tc_kernel<D><<<dim3(items, a.Hk, a.B), kThreads, KvLayout<D>::BYTES, stream>>>(a, plan, mq, mk, mv, mg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    dq_tc_kernel<D><<<dim3((a.T + 127) / 128, a.Hq, a.B), kThreads, QLayout<D>::BYTES, stream>>>(a, mq, mk, mv, mg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (plan.nseg && plan.nsink) {
+        sink_sum_kernel<D><<<dim3(plan.nsink * 16, a.Hk, a.B), 256, 0, stream>>>(a, plan);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t swa_bwd_tc_partial_floats(const SwaArgs &a, int num_sms)
+{
+    const KvPlan p = plan_kv(a, num_sms);
+    return p.nseg ? (size_t)a.B * a.Hk * p.nsink * p.nseg * 256 * a.d : 0;
+}
+
+cudaError_t launch_swa_bwd_tc(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
+{
+    return a.d == 128 ? impl<128>(a, part, num_sms, stream) : impl<64>(a, part, num_sms, stream);
+}
+
+}  // namespace gdn2

@@ -384,9 +384,8 @@ cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t stream)
     return a.d == 128 ? fwd_impl<float, 128>(a, stream) : fwd_impl<float, 64>(a, stream);
 }
 
-cudaError_t launch_swa_bwd_simt(const SwaArgs &a, bool bf16, cudaStream_t stream)
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t stream)
 {
-    if (bf16) return a.d == 128 ? bwd_impl<__nv_bfloat16, 128>(a, stream) : bwd_impl<__nv_bfloat16, 64>(a, stream);
     return a.d == 128 ? bwd_impl<float, 128>(a, stream) : bwd_impl<float, 64>(a, stream);
 }
 
