@@ -74,9 +74,10 @@ struct NormArgs {
     float *partial;                  // norm_bwd_partial_floats(...) of workspace
     long long N;
     int D;
+    unsigned int *err;               // device error word
 };
 cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16, int num_sms, cudaStream_t stream);
-size_t norm_bwd_partial_floats(long long N, int D, int num_sms);
+size_t norm_bwd_partial_floats(long long N, int D, bool bf16, int num_sms);
 cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16, int num_sms, cudaStream_t stream);
 
 }  // namespace gdn2

@@ -268,6 +268,7 @@ extern "C" gdn2_status gdn2_block_norm_fwd(const void *r, const void *y, const v
     unsigned int *err = nullptr;
     int sms = 0;
     if (!device_info(&err, &sms)) return GDN2_ERR_CUDA;
+    a.err = err;
     return from_cuda(launch_norm_fwd(a, dtype == GDN2_BF16, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -303,9 +304,10 @@ extern "C" gdn2_status gdn2_block_norm_bwd(const void *r, const void *y, const v
     cudaMemPool_t pool = workspace_pool(dev);
     if (!pool) return GDN2_ERR_CUDA;
     void *ws = nullptr;
-    if (cudaMallocFromPoolAsync(&ws, sizeof(float) * norm_bwd_partial_floats(N, D, sms), pool, s) != cudaSuccess)
+    if (cudaMallocFromPoolAsync(&ws, sizeof(float) * norm_bwd_partial_floats(N, D, dtype == GDN2_BF16, sms), pool, s) != cudaSuccess)
         return GDN2_ERR_CUDA;
     a.partial = static_cast<float *>(ws);
+    a.err = err;
     const cudaError_t e = launch_norm_bwd(a, dtype == GDN2_BF16, sms, s);
     const cudaError_t fe = cudaFreeAsync(ws, s);
     return from_cuda(e == cudaSuccess ? fe : e);
