@@ -86,6 +86,18 @@ bool make_token_map(CUtensorMap *m, const void *base, int d, int H, int T, int B
     return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, H, T, B, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool make_plane_map(CUtensorMap *m, const void *base, bool bf16, long long cols, long long rows, int box_c, int box_r)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * (bf16 ? 2 : 4)};
+    cuuint32_t box[2] = {(cuuint32_t)box_c, (cuuint32_t)box_r}, estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_rows_map(CUtensorMap *m, const void *base, int d, int H, int T, int B, const long long (&st)[3], int box_t)
 {
     return make_strided_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, H, T, B, st, 64, box_t,

@@ -57,6 +57,7 @@ struct ScanArgs {
     float *dla;
     float *dh0;                      // may be null
     int B, T, C;
+    unsigned int *err;               // device error word
 };
 cudaError_t launch_scan_fwd(const ScanArgs &a, bool bf16, int num_sms, cudaStream_t stream);
 cudaError_t launch_scan_bwd(const ScanArgs &a, bool bf16, int num_sms, cudaStream_t stream);

@@ -200,6 +200,7 @@ extern "C" gdn2_status gdn2_scan_fwd(const void *x, const void *w, const float *
     unsigned int *err = nullptr;
     int sms = 0;
     if (!device_info(&err, &sms)) return GDN2_ERR_CUDA;
+    a.err = err;
     return from_cuda(launch_scan_fwd(a, dtype == GDN2_BF16, sms, s));
 }
 
@@ -225,6 +226,7 @@ extern "C" gdn2_status gdn2_scan_bwd(const void *x, const void *w, const float *
     unsigned int *err = nullptr;
     int sms = 0;
     if (!device_info(&err, &sms)) return GDN2_ERR_CUDA;
+    a.err = err;
     return from_cuda(launch_scan_bwd(a, dtype == GDN2_BF16, sms, s));
 }
 

@@ -110,6 +110,8 @@ bool make_input_maps(const FwdArgs &a, CUtensorMap *maps);
 bool make_token_map(CUtensorMap *m, const void *base, int d, int H, int T, int B);
 // The same with element strides {batch, token, head} and boxes of box_t tokens.
 bool make_rows_map(CUtensorMap *m, const void *base, int d, int H, int T, int B, const long long (&st)[3], int box_t);
+// A dense [rows][cols] tensor (bf16 or fp32) in unswizzled boxes of box_r rows x box_c columns.
+bool make_plane_map(CUtensorMap *m, const void *base, bool bf16, long long cols, long long rows, int box_c, int box_r);
 cudaError_t launch_fwd_tc(const FwdArgs &a);
 // `overlap`: launch as a programmatic dependent of the previous kernel in the
 // stream, so that it may start before that kernel ends (only where the two

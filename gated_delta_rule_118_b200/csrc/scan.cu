@@ -1,30 +1,37 @@
 // scan.cu -- the gated linear recurrence h_t = alpha_t h_{t-1} + w_t x_t per
 // channel: forward, backward and single step.
 //
-// One pass over the data.  A CTA takes 64 channels and 128 tokens at a time: its eight
+// One pass over the data.  A CTA takes 64 channels and 64 tokens at a time: its four
 // warps hold 16 tokens each in registers (two channels a lane), reduce them to the map
 // h -> A h + H of their span, and compose the maps of the spans before theirs through
 // shared memory; then every warp knows the state it starts from and runs its tokens.
 // When channels alone do not fill the device, a cluster of up to eight CTAs takes
-// consecutive spans of 128 tokens of the same channels and exchanges its maps through
-// distributed shared memory.  The walk over the sequence carries the state in registers.
+// consecutive spans of 64 tokens of the same channels and exchanges its maps through
+// distributed shared memory.  The walk over the sequence carries the state in registers,
+// and the next spans' tiles arrive by TMA meanwhile (two CTAs an SM; channel counts that
+// TMA cannot address, whose rows are not a multiple of 16 bytes, take plain loads).
 // Bound by HBM.
 //
 // Backward: the same with time reversed, on c_t = alpha_t g_t (the gradient that leaves a
 // token towards the past): c -> A c + G.  h_{t-1} comes from the forward's checkpoints,
 // one per 16 tokens, recomputed in fp32.
 #include <cooperative_groups.h>
+#include <cuda.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "hybrid.h"
+#include "launch.h"
 #include "packed.cuh"
+#include "sm100.cuh"
 
 namespace gdn2 {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTok = kScanBlock;          // tokens of a warp
 constexpr int kSpan = kWarps * kTok;      // tokens of a CTA
 constexpr int kChan = 64;                 // channels of a CTA
@@ -89,7 +96,8 @@ __device__ __forceinline__ f2 enter_span(Maps &m, int parity, int order, f2 A, f
     if constexpr (CL) {
         cg::cluster_group cluster = cg::this_cluster();
         const int size = cluster.num_blocks(), rank = cluster.block_rank();
-        if (order < size) *cluster.map_shared_rank(&m.cta[parity][rank][lane], order) = make_ulonglong2(ta, th);
+        for (int p = order; p < size; p += kWarps)
+            *cluster.map_shared_rank(&m.cta[parity][rank][lane], p) = make_ulonglong2(ta, th);
         cluster.sync();
         f2 s = state;
         for (int r = 0; r < size; ++r) {
@@ -111,31 +119,80 @@ struct Place {
         : c((int)(blockIdx.x / csize) * kChan + 2 * (threadIdx.x & 31)), b(blockIdx.y), rank(blockIdx.x % csize), size(csize) {}
 };
 
-template <typename E, bool EVEN, bool CL>
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, int csize)
+// How a kernel gets its rows: element by element, pairs, or tiles by TMA.
+enum Source { kOdd, kEven, kTile };
+
+// One span's tiles in shared memory: log_alpha, then x, w (and dy), [64 tokens][64 channels].
+template <typename E, int NE>
+struct Stage {
+    static constexpr int LA = 0, TILE = kSpan * kChan;
+    static constexpr int BYTES = TILE * 4 + NE * TILE * (int)sizeof(E);
+    static constexpr int COUNT = NE == 2 ? (sizeof(E) == 2 ? 3 : 2) : (sizeof(E) == 2 ? 2 : 1);  // stages of a CTA
+    static constexpr int el(int k) { return TILE * 4 + k * TILE * (int)sizeof(E); }
+};
+struct SpanMaps {
+    CUtensorMap la, e[3];
+};
+template <typename E, int NE>
+__device__ __forceinline__ void fetch_span(uint8_t *st, const SpanMaps &m, uint64_t *bar, int c, long long row)
 {
+    using S = Stage<E, NE>;
+    sm100::mbar_arrive_expect_tx(bar, S::BYTES);
+    sm100::tma_load_2d(st + S::LA, &m.la, bar, c, (int)row);
+#pragma unroll
+    for (int k = 0; k < NE; ++k) sm100::tma_load_2d(st + S::el(k), &m.e[k], bar, c, (int)row);
+}
+
+// Token t (of the warp's 16) of a tensor: from the stage, or from memory.
+template <Source SRC, typename T>
+__device__ __forceinline__ f2 take(const uint8_t *tile, const T *row, int warp_row, int t, int c, int C)
+{
+    if constexpr (SRC == kTile) return pair_of(reinterpret_cast<const T *>(tile) + (warp_row + t) * kChan + 2 * (threadIdx.x & 31));
+    else return load_pair<SRC == kEven>(row + (long long)t * C, c, C);
+}
+
+template <typename E, Source SRC, bool CL>
+__global__ void __launch_bounds__(kThreads, 2)
+scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm)
+{
+    using S = Stage<E, 2>;
+    constexpr bool EVEN = SRC != kOdd;
+    extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Maps maps;
+    __shared__ __align__(8) uint64_t full[S::COUNT];
     const Place pl(csize);
-    const int warp = threadIdx.x >> 5, c = pl.c;
-    const long long seq = (long long)pl.b * a.T;
+    const int warp = threadIdx.x >> 5, c = pl.c, c_cta = (int)(blockIdx.x / csize) * kChan;
+    const long long seq = (long long)pl.b * a.T, step = (long long)kSpan * pl.size;
     const int nblk = (a.T + kTok - 1) / kTok;
+    if (SRC == kTile && threadIdx.x == 0) {
+        for (int i = 0; i < S::COUNT; ++i) sm100::mbar_init(full + i, 1);
+        sm100::fence_mbar_init();
+        for (int i = 0; i < S::COUNT; ++i)
+            if (i * step < a.T) fetch_span<E, 2>(dyn + i * S::BYTES, tm, full + i, c_cta, seq + i * step + pl.rank * kSpan);
+    }
     f2 state = a.h0 ? load_pair<EVEN>(a.h0 + (long long)pl.b * a.C, c, a.C) : 0;
+    __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read h0, which h_T may alias)
-    int parity = 0;
-    for (long long s0 = 0; s0 < a.T; s0 += (long long)kSpan * pl.size, parity ^= 1) {
+    int parity = 0, st = 0;
+    uint32_t ph = 0;
+    for (long long s0 = 0; s0 < a.T; s0 += step, parity ^= 1) {
         const long long t0 = s0 + pl.rank * kSpan + warp * kTok;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
         const long long row = (seq + t0) * a.C;
-        f2 al[kTok], u[kTok];
+        const uint8_t *tile = dyn + st * S::BYTES;
+        if (SRC == kTile) sm100::mbar_wait(full + st, ph, a.err);
+        f2 al[kTok], u[kTok], A = both(1.f), H = 0;
+        auto gather = [&](auto whole) {
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const long long at = row + (long long)t * a.C;
-            const bool on = t < live;
-            al[t] = on ? load_pair<EVEN>(a.la + at, c, a.C) : 0;
-            u[t] = on ? mul2(load_pair<EVEN>(static_cast<const E *>(a.x) + at, c, a.C),
-                             load_pair<EVEN>(static_cast<const E *>(a.w) + at, c, a.C)) : 0;
-        }
-        f2 A = both(1.f), H = 0;
+            for (int t = 0; t < kTok; ++t) {
+                const bool on = decltype(whole)::value || t < live;
+                al[t] = on ? take<SRC>(tile + S::LA, a.la + row, warp * kTok, t, c, a.C) : 0;
+                u[t] = on ? mul2(take<SRC>(tile + S::el(0), static_cast<const E *>(a.x) + row, warp * kTok, t, c, a.C),
+                                 take<SRC>(tile + S::el(1), static_cast<const E *>(a.w) + row, warp * kTok, t, c, a.C)) : 0;
+            }
+        };
+        if (live == kTok) gather(std::true_type());
+        else gather(std::false_type());
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
             al[t] = exp_pair(al[t]);
@@ -143,70 +200,107 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             H = fma2(al[t], H, u[t]);
         }
         f2 h = enter_span<CL>(maps, parity, warp, A, H, state);
-        if (live > 0) {
-            if (a.ckpt) store_pair<EVEN>(a.ckpt + ((long long)pl.b * nblk + t0 / kTok) * a.C, c, a.C, h);
+        if (SRC == kTile) {  // (behind the barrier of enter_span: every warp has its tokens in registers)
+            if (threadIdx.x == 0 && s0 + S::COUNT * step < a.T)
+                fetch_span<E, 2>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + s0 + S::COUNT * step + pl.rank * kSpan);
+            if (++st == S::COUNT) st = 0, ph ^= 1;
+        }
+        if (live > 0 && a.ckpt) store_pair<EVEN>(a.ckpt + ((long long)pl.b * nblk + t0 / kTok) * a.C, c, a.C, h);
+        E *y = static_cast<E *>(a.y) + row;
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                h = fma2(al[t], h, u[t]);
-                if (t < live) store_pair<EVEN>(static_cast<E *>(a.y) + row + (long long)t * a.C, c, a.C, h);
-            }
+        for (int t = 0; t < kTok; ++t) {
+            h = fma2(al[t], h, u[t]);
+            if (t < live) store_pair<EVEN>(y, c, a.C, h);
+            y += a.C;
         }
     }
     if (a.h_T && warp == 0 && pl.rank == 0) store_pair<EVEN>(a.h_T + (long long)pl.b * a.C, c, a.C, state);
 }
 
-template <typename E, bool EVEN, bool CL>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a, int csize)
+template <typename E, Source SRC, bool CL>
+__global__ void __launch_bounds__(kThreads, 2)
+scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm)
 {
+    using S = Stage<E, 3>;
+    constexpr bool EVEN = SRC != kOdd;
+    extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Maps maps;
+    __shared__ __align__(8) uint64_t full[S::COUNT], empty[S::COUNT];
     const Place pl(csize);
-    const int warp = threadIdx.x >> 5, c = pl.c;
-    const long long seq = (long long)pl.b * a.T;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = pl.c, c_cta = (int)(blockIdx.x / csize) * kChan;
+    const long long seq = (long long)pl.b * a.T, step = (long long)kSpan * pl.size, spans = (a.T + step - 1) / step;
     const int nblk = (a.T + kTok - 1) / kTok;
+    // along the walk the last tokens come first: rank 0 and warp 0 take the latest
+    auto first_token = [&](long long sp) { return sp * step + (pl.size - 1 - pl.rank) * kSpan; };
+    if (SRC == kTile && threadIdx.x == 0) {
+        for (int i = 0; i < S::COUNT; ++i) {
+            sm100::mbar_init(full + i, 1);
+            sm100::mbar_init(empty + i, kWarps);
+        }
+        sm100::fence_mbar_init();
+        for (int i = 0; i < S::COUNT && i < spans; ++i)
+            fetch_span<E, 3>(dyn + i * S::BYTES, tm, full + i, c_cta, seq + first_token(spans - 1 - i));
+    }
     f2 state = a.dh_T ? load_pair<EVEN>(a.dh_T + (long long)pl.b * a.C, c, a.C) : 0;
+    __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read dh_T, which dh0 may alias)
-    int parity = 0;
-    const long long step = (long long)kSpan * pl.size, spans = (a.T + step - 1) / step;
+    int parity = 0, st = 0;
+    uint32_t ph = 0;
     for (long long sp = spans - 1; sp >= 0; --sp, parity ^= 1) {
-        // along the walk the last tokens come first: rank 0 and warp 0 take the latest
-        const long long t0 = sp * step + (pl.size - 1 - pl.rank) * kSpan + (kWarps - 1 - warp) * kTok;
+        const int wrow = (kWarps - 1 - warp) * kTok;
+        const long long t0 = first_token(sp) + wrow;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
         const long long row = (seq + t0) * a.C;
-        const E *x = static_cast<const E *>(a.x) + row, *w = static_cast<const E *>(a.w) + row;
-        f2 al[kTok], hp[kTok], dy[kTok];
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const long long at = (long long)t * a.C;
-            const bool on = t < live;
-            al[t] = on ? load_pair<EVEN>(a.la + row + at, c, a.C) : 0;
-            dy[t] = on ? load_pair<EVEN>(static_cast<const E *>(a.dy) + row + at, c, a.C) : 0;
-            hp[t] = on ? mul2(load_pair<EVEN>(x + at, c, a.C), load_pair<EVEN>(w + at, c, a.C)) : 0;
-        }
+        const E *x = static_cast<const E *>(a.x) + row, *w = static_cast<const E *>(a.w) + row, *dy = static_cast<const E *>(a.dy) + row;
+        const uint8_t *tile = dyn + st * S::BYTES;
         f2 h = live ? load_pair<EVEN>(a.ckpt + ((long long)pl.b * nblk + t0 / kTok) * a.C, c, a.C) : 0;
+        if (SRC == kTile) sm100::mbar_wait(full + st, ph, a.err);
+        // x, w and dy are taken twice (from the stage, or from cache): kept in registers they
+        // would halve the warps of an SM
+        auto get = [&](int k, const E *p, int t) { return take<SRC>(tile + S::el(k), p, wrow, t, c, a.C); };
+        f2 al[kTok], hp[kTok], A = both(1.f), G = 0;
+        auto gather = [&](auto whole) {
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            al[t] = exp_pair(al[t]);
-            const f2 next = fma2(al[t], h, hp[t]);
-            hp[t] = h;
-            h = next;
-        }
-        f2 A = both(1.f), G = 0;
+            for (int t = 0; t < kTok; ++t) {
+                const bool on = decltype(whole)::value || t < live;
+                al[t] = on ? exp_pair(take<SRC>(tile + S::LA, a.la + row, wrow, t, c, a.C)) : both(1.f);
+                hp[t] = h;
+                if (on) h = fma2(al[t], h, mul2(get(0, x, t), get(1, w, t)));
+            }
 #pragma unroll
-        for (int t = kTok - 1; t >= 0; --t) {
-            A = mul2(al[t], A);
-            G = mul2(al[t], add2(dy[t], G));
-        }
+            for (int t = kTok - 1; t >= 0; --t) {
+                const bool on = decltype(whole)::value || t < live;
+                A = mul2(al[t], A);
+                G = mul2(al[t], on ? add2(get(2, dy, t), G) : G);
+            }
+        };
+        if (live == kTok) gather(std::true_type());
+        else gather(std::false_type());
         f2 g = enter_span<CL>(maps, parity, warp, A, G, state);
+        E *dx = static_cast<E *>(a.dx) + row, *dw = static_cast<E *>(a.dw) + row;
+        float *dla = a.dla + row;
+        auto sweep = [&](auto whole) {
 #pragma unroll
-        for (int t = kTok - 1; t >= 0; --t) {
-            if (t >= live) continue;
-            const long long at = (long long)t * a.C;
-            g = add2(dy[t], g);
-            // (x and w again, from cache: kept in registers they would halve the CTAs of an SM)
-            store_pair<EVEN>(static_cast<E *>(a.dx) + row + at, c, a.C, mul2(g, load_pair<EVEN>(w + at, c, a.C)));
-            store_pair<EVEN>(static_cast<E *>(a.dw) + row + at, c, a.C, mul2(g, load_pair<EVEN>(x + at, c, a.C)));
-            g = mul2(g, al[t]);
-            store_pair<EVEN>(a.dla + row + at, c, a.C, mul2(g, hp[t]));
+            for (int t = kTok - 1; t >= 0; --t) {
+                if (!decltype(whole)::value && t >= live) continue;
+                const long long at = (long long)t * a.C;
+                g = add2(get(2, dy, t), g);
+                store_pair<EVEN>(dx + at, c, a.C, mul2(g, get(1, w, t)));
+                store_pair<EVEN>(dw + at, c, a.C, mul2(g, get(0, x, t)));
+                g = mul2(g, al[t]);
+                store_pair<EVEN>(dla + at, c, a.C, mul2(g, hp[t]));
+            }
+        };
+        if (live == kTok) sweep(std::true_type());
+        else sweep(std::false_type());
+        if (SRC == kTile) {
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(empty + st);
+            if (threadIdx.x == 0 && sp >= S::COUNT) {
+                sm100::mbar_wait(empty + st, ph, a.err);
+                fetch_span<E, 3>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + first_token(sp - S::COUNT));
+            }
+            if (++st == S::COUNT) st = 0, ph ^= 1;
         }
     }
     if (a.dh0 && warp == 0 && pl.rank == 0) store_pair<EVEN>(a.dh0 + (long long)pl.b * a.C, c, a.C, state);
@@ -250,11 +344,15 @@ int cluster_size(const ScanArgs &a, int num_sms)
 }
 
 template <auto kern>
-cudaError_t launch(const ScanArgs &a, int cs, cudaStream_t stream)
+cudaError_t launch(const ScanArgs &a, int cs, int smem, const SpanMaps &tm, cudaStream_t stream)
 {
+    static std::atomic<unsigned long long> set{0};
+    cudaError_t e = ensure_smem_limit(kern, smem, set);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((a.C + kChan - 1) / kChan) * cs, a.B);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -262,34 +360,81 @@ cudaError_t launch(const ScanArgs &a, int cs, cudaStream_t stream)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a, cs);
+    return cudaLaunchKernelEx(&cfg, kern, a, cs, tm);
 }
 
-template <typename E, bool EVEN>
+// Tiles by TMA need rows of a multiple of 16 bytes and row numbers that fit its coordinates.
+template <typename E>
+Source source_of(const ScanArgs &a)
+{
+    if (a.C % (16 / sizeof(E)) == 0 && (long long)a.B * a.T + kSpan * kMaxCluster < 0x7fffffffLL) return kTile;
+    return a.C % 2 == 0 ? kEven : kOdd;
+}
+
+template <typename E, Source SRC>
 cudaError_t fwd_impl(const ScanArgs &a, int num_sms, cudaStream_t stream)
 {
     const int cs = cluster_size(a, num_sms);
-    return cs > 1 ? launch<scan_fwd_kernel<E, EVEN, true>>(a, cs, stream) : launch<scan_fwd_kernel<E, EVEN, false>>(a, 1, stream);
+    SpanMaps tm{};
+    int smem = 0;
+    if (SRC == kTile) {
+        const long long rows = (long long)a.B * a.T;
+        const bool bf16 = sizeof(E) == 2;
+        smem = Stage<E, 2>::BYTES * Stage<E, 2>::COUNT;
+        if (!make_plane_map(&tm.la, a.la, false, a.C, rows, kChan, kSpan) || !make_plane_map(&tm.e[0], a.x, bf16, a.C, rows, kChan, kSpan) ||
+            !make_plane_map(&tm.e[1], a.w, bf16, a.C, rows, kChan, kSpan))
+            return cudaErrorInvalidValue;
+    }
+    return cs > 1 ? launch<scan_fwd_kernel<E, SRC, true>>(a, cs, smem, tm, stream)
+                  : launch<scan_fwd_kernel<E, SRC, false>>(a, 1, smem, tm, stream);
 }
-template <typename E, bool EVEN>
+template <typename E, Source SRC>
 cudaError_t bwd_impl(const ScanArgs &a, int num_sms, cudaStream_t stream)
 {
     const int cs = cluster_size(a, num_sms);
-    return cs > 1 ? launch<scan_bwd_kernel<E, EVEN, true>>(a, cs, stream) : launch<scan_bwd_kernel<E, EVEN, false>>(a, 1, stream);
+    SpanMaps tm{};
+    int smem = 0;
+    if (SRC == kTile) {
+        const long long rows = (long long)a.B * a.T;
+        const bool bf16 = sizeof(E) == 2;
+        smem = Stage<E, 3>::BYTES * Stage<E, 3>::COUNT;
+        if (!make_plane_map(&tm.la, a.la, false, a.C, rows, kChan, kSpan) || !make_plane_map(&tm.e[0], a.x, bf16, a.C, rows, kChan, kSpan) ||
+            !make_plane_map(&tm.e[1], a.w, bf16, a.C, rows, kChan, kSpan) || !make_plane_map(&tm.e[2], a.dy, bf16, a.C, rows, kChan, kSpan))
+            return cudaErrorInvalidValue;
+    }
+    return cs > 1 ? launch<scan_bwd_kernel<E, SRC, true>>(a, cs, smem, tm, stream)
+                  : launch<scan_bwd_kernel<E, SRC, false>>(a, 1, smem, tm, stream);
+}
+
+template <typename E>
+cudaError_t fwd_by_source(const ScanArgs &a, int num_sms, cudaStream_t stream)
+{
+    switch (source_of<E>(a)) {
+    case kTile: return fwd_impl<E, kTile>(a, num_sms, stream);
+    case kEven: return fwd_impl<E, kEven>(a, num_sms, stream);
+    default: return fwd_impl<E, kOdd>(a, num_sms, stream);
+    }
+}
+template <typename E>
+cudaError_t bwd_by_source(const ScanArgs &a, int num_sms, cudaStream_t stream)
+{
+    switch (source_of<E>(a)) {
+    case kTile: return bwd_impl<E, kTile>(a, num_sms, stream);
+    case kEven: return bwd_impl<E, kEven>(a, num_sms, stream);
+    default: return bwd_impl<E, kOdd>(a, num_sms, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, bool bf16, int num_sms, cudaStream_t stream)
 {
-    if (a.C % 2 == 0) return bf16 ? fwd_impl<__nv_bfloat16, true>(a, num_sms, stream) : fwd_impl<float, true>(a, num_sms, stream);
-    return bf16 ? fwd_impl<__nv_bfloat16, false>(a, num_sms, stream) : fwd_impl<float, false>(a, num_sms, stream);
+    return bf16 ? fwd_by_source<__nv_bfloat16>(a, num_sms, stream) : fwd_by_source<float>(a, num_sms, stream);
 }
 
 cudaError_t launch_scan_bwd(const ScanArgs &a, bool bf16, int num_sms, cudaStream_t stream)
 {
-    if (a.C % 2 == 0) return bf16 ? bwd_impl<__nv_bfloat16, true>(a, num_sms, stream) : bwd_impl<float, true>(a, num_sms, stream);
-    return bf16 ? bwd_impl<__nv_bfloat16, false>(a, num_sms, stream) : bwd_impl<float, false>(a, num_sms, stream);
+    return bf16 ? bwd_by_source<__nv_bfloat16>(a, num_sms, stream) : bwd_by_source<float>(a, num_sms, stream);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, float *h, bool bf16, cudaStream_t stream)
