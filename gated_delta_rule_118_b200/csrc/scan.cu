@@ -74,13 +74,15 @@ __device__ __forceinline__ f2 exp_pair(f2 v)
 struct Maps {
     ulonglong2 warp[2][kWarps][32];       // [parity][warp][lane] {A, H}
     ulonglong2 cta[2][kMaxCluster][32];   // [parity][CTA][lane]
+    uint64_t landed[2];                   // [parity]: every CTA's map is here
 };
 // From this warp's map and the running state: the state entering its span; `state`
 // becomes the one behind the whole cluster's span.  `order` is the warp's (or the CTA's)
 // position along the walk.
 template <bool CL>
-__device__ __forceinline__ f2 enter_span(Maps &m, int parity, int order, f2 A, f2 H, f2 &state)
+__device__ __forceinline__ f2 enter_span(Maps &m, int step, int order, f2 A, f2 H, f2 &state, unsigned int *err)
 {
+    const int parity = step & 1;
     const int lane = threadIdx.x & 31;
     m.warp[parity][order][lane] = make_ulonglong2(A, H);
     __syncthreads();
@@ -94,11 +96,17 @@ __device__ __forceinline__ f2 enter_span(Maps &m, int parity, int order, f2 A, f
     }
     f2 in = state;
     if constexpr (CL) {
+        // each CTA sends its map to all and waits for theirs: 16 bytes a lane that signal the
+        // receiver's barrier (1 x 65536 x 2048 bf16: 245 us, against 332 us with a barrier of
+        // the whole cluster).  A CTA that sends for step k + 2 has this CTA's map of k + 1,
+        // sent when its k was read.
         cg::cluster_group cluster = cg::this_cluster();
         const int size = cluster.num_blocks(), rank = cluster.block_rank();
+        if (threadIdx.x == 0) sm100::mbar_arrive_expect_tx(m.landed + parity, size * 512);
         for (int p = order; p < size; p += kWarps)
-            *cluster.map_shared_rank(&m.cta[parity][rank][lane], p) = make_ulonglong2(ta, th);
-        cluster.sync();
+            sm100::st_async_16(sm100::peer_smem(&m.cta[parity][rank][lane], p), make_ulonglong2(ta, th),
+                               sm100::peer_smem(m.landed + parity, p));
+        sm100::mbar_wait(m.landed + parity, (step >> 1) & 1, err);
         f2 s = state;
         for (int r = 0; r < size; ++r) {
             if (r == rank) in = s;
@@ -170,12 +178,16 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         for (int i = 0; i < S::COUNT; ++i)
             if (i * step < a.T) fetch_span<E, 2>(dyn + i * S::BYTES, tm, full + i, c_cta, seq + i * step + pl.rank * kSpan);
     }
+    if (CL && threadIdx.x < 2) {
+        sm100::mbar_init(maps.landed + threadIdx.x, 1);
+        sm100::fence_mbar_init();
+    }
     f2 state = a.h0 ? load_pair<EVEN>(a.h0 + (long long)pl.b * a.C, c, a.C) : 0;
     __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read h0, which h_T may alias)
-    int parity = 0, st = 0;
+    int k = 0, st = 0;
     uint32_t ph = 0;
-    for (long long s0 = 0; s0 < a.T; s0 += step, parity ^= 1) {
+    for (long long s0 = 0; s0 < a.T; s0 += step, ++k) {
         const long long t0 = s0 + pl.rank * kSpan + warp * kTok;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
         const long long row = (seq + t0) * a.C;
@@ -199,7 +211,7 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
             A = mul2(al[t], A);
             H = fma2(al[t], H, u[t]);
         }
-        f2 h = enter_span<CL>(maps, parity, warp, A, H, state);
+        f2 h = enter_span<CL>(maps, k, warp, A, H, state, a.err);
         if (SRC == kTile) {  // (behind the barrier of enter_span: every warp has its tokens in registers)
             if (threadIdx.x == 0 && s0 + S::COUNT * step < a.T)
                 fetch_span<E, 2>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + s0 + S::COUNT * step + pl.rank * kSpan);
@@ -241,12 +253,16 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         for (int i = 0; i < S::COUNT && i < spans; ++i)
             fetch_span<E, 3>(dyn + i * S::BYTES, tm, full + i, c_cta, seq + first_token(spans - 1 - i));
     }
+    if (CL && threadIdx.x < 2) {
+        sm100::mbar_init(maps.landed + threadIdx.x, 1);
+        sm100::fence_mbar_init();
+    }
     f2 state = a.dh_T ? load_pair<EVEN>(a.dh_T + (long long)pl.b * a.C, c, a.C) : 0;
     __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read dh_T, which dh0 may alias)
-    int parity = 0, st = 0;
+    int k = 0, st = 0;
     uint32_t ph = 0;
-    for (long long sp = spans - 1; sp >= 0; --sp, parity ^= 1) {
+    for (long long sp = spans - 1; sp >= 0; --sp, ++k) {
         const int wrow = (kWarps - 1 - warp) * kTok;
         const long long t0 = first_token(sp) + wrow;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
@@ -276,7 +292,7 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         };
         if (live == kTok) gather(std::true_type());
         else gather(std::false_type());
-        f2 g = enter_span<CL>(maps, parity, warp, A, G, state);
+        f2 g = enter_span<CL>(maps, k, warp, A, G, state, a.err);
         E *dx = static_cast<E *>(a.dx) + row, *dw = static_cast<E *>(a.dw) + row;
         float *dla = a.dla + row;
         auto sweep = [&](auto whole) {

@@ -215,6 +215,22 @@ __device__ __forceinline__ void allow_dependent_launch() { asm volatile("griddep
 // completed and its memory operations are visible (returns at once otherwise).
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ---------------------------------------------------------------- cluster shared memory
+// The address of `p` (of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+// 16 bytes into a peer's shared memory, completing 16 on the peer's mbarrier.
+__device__ __forceinline__ void st_async_16(uint32_t addr, ulonglong2 v, uint32_t bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "l"(v.x), "l"(v.y), "r"(bar)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- cluster launch control
 // Ask for a CTA of this grid that has not started yet, to run its work here instead:
 // 16 bytes arrive in `response` and complete on `bar` (after mbar_arrive_expect_tx of

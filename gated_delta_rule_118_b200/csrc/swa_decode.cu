@@ -1,9 +1,19 @@
 // swa_decode.cu -- one token of the windowed attention against a ring cache.
 //
-// A cluster of CTAs shares one (batch, key/value head): each CTA takes a run of
-// the visible positions, each of its warps every fourth group of them, and the
-// partial (max, sum, output) triples are joined through shared memory, then
-// through distributed shared memory -- one launch, no workspace.
+// A cluster of CTAs shares one (batch, key/value head): each CTA takes a run of the
+// visible positions, each of its warps every fourth group of them, and the partial (max,
+// sum, output) triples are joined through shared memory, then through distributed shared
+// memory -- one launch, no workspace.  Bound by HBM: the visible cache is read once for
+// all query heads of the group.
+//
+// bf16: warp-level matrix instructions over 16 heads x 16 keys.  Keys and values go from
+// memory straight into operand registers, 16 bytes a load: a dot product does not care in
+// which order its channels are taken, so a lane's 16 bytes of a key serve as two k-steps
+// of it (the query is loaded in the same order), and an output tile takes every eighth
+// channel so that a lane's 16 bytes of a value row feed eight tiles.  (The fifth-generation
+// tensor core would need the rows in shared memory first; a step of 16 keys is 64 warp
+// instructions here against 8 KB from memory, so it would not be used a tenth.)
+// fp32: one key row per half or whole warp on the CUDA cores.
 #include <cooperative_groups.h>
 
 #include "launch.h"
@@ -16,6 +26,7 @@ using namespace swa;
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
+constexpr long long kFill = 8;  // CTAs per SM that the split of the positions aims at
 
 // Visible positions in order (sinks behind the window, then the window) -> cache slots.
 struct Visible {
@@ -50,14 +61,69 @@ __device__ __forceinline__ void put_new_token(const SwaDecodeArgs &a, int b, int
     }
 }
 
+// The warps' partial results of a CTA, and the CTA's.
+template <int GC, int D>
+struct Partials {
+    float m[kWarps][GC], l[kWarps][GC];
+    alignas(16) float o[kWarps][GC][D];
+};
+template <int GC, int D>
+struct Joined {
+    float m[GC], l[GC], o[GC][D];
+};
+
+// Joins the warps, then the CTAs of the cluster, and writes the heads [0, ng).
+template <typename E, int D, int GC>
+__device__ __forceinline__ void join(const Partials<GC, D> &part, Joined<GC, D> &mine, E *out, int split, int nsplit, int ng)
+{
+    __syncthreads();
+    for (int i = threadIdx.x; i < ng * D; i += blockDim.x) {
+        const int g = i / D, d = i % D;
+        float mn = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mn = fmaxf(mn, part.m[w][g]);
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        float sl = 0.f, so = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2f(part.m[w][g] - ms);
+            sl = fmaf(part.l[w][g], f, sl);
+            so = fmaf(part.o[w][g][d], f, so);
+        }
+        if (nsplit == 1) {
+            out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
+        } else {
+            mine.o[g][d] = so;
+            if (d == 0) mine.m[g] = mn, mine.l[g] = sl;
+        }
+    }
+    if (nsplit == 1) return;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int g = split; g < ng; g += nsplit)  // heads dealt to the CTAs of the cluster
+        for (int d = threadIdx.x; d < D; d += blockDim.x) {
+            float mn = -INFINITY;
+            for (int r = 0; r < nsplit; ++r) mn = fmaxf(mn, *cluster.map_shared_rank(&mine.m[g], r));
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            float sl = 0.f, so = 0.f;
+            for (int r = 0; r < nsplit; ++r) {
+                const float f = exp2f(*cluster.map_shared_rank(&mine.m[g], r) - ms);
+                sl = fmaf(*cluster.map_shared_rank(&mine.l[g], r), f, sl);
+                so = fmaf(*cluster.map_shared_rank(&mine.o[g][d], r), f, so);
+            }
+            out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
+        }
+    cluster.sync();
+}
+
 // GC query heads of the group per CTA; lanes hold 4 channels each of D / 4 lanes per key.
 template <typename E, int D, int GC>
 __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
 {
     constexpr int LPR = D / 4, KPW = 32 / LPR;  // lanes per key, keys per warp step
     constexpr int U = 4;                        // steps in flight
-    __shared__ float sm_m[kWarps][GC], sm_l[kWarps][GC], sm_o[kWarps][GC][D];
-    __shared__ float cm[GC], cl[GC], co[GC][D];
+    __shared__ Partials<GC, D> part;
+    __shared__ Joined<GC, D> joined;
     const int split = blockIdx.x, hk = blockIdx.y / nchunk, chunk = blockIdx.y % nchunk, b = blockIdx.z;
     const int G = a.Hq / a.Hk, g0 = chunk * GC, ng = min(GC, G - g0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, x = lane % LPR * 4;
@@ -127,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs
             }
         }
     }
-    // the keys of a warp's sub-rows, then the warps, then the CTAs of the cluster
+    // the keys of a warp's sub-rows
 #pragma unroll
     for (int g = 0; g < GC; ++g) {
 #pragma unroll
@@ -141,55 +207,202 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs
         }
         if (lane < LPR) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sm_o[warp][g][x + c] = o[g][c];
-            if (lane == 0) sm_m[warp][g] = m[g], sm_l[warp][g] = l[g];
+            for (int c = 0; c < 4; ++c) part.o[warp][g][x + c] = o[g][c];
+            if (lane == 0) part.m[warp][g] = m[g], part.l[warp][g] = l[g];
         }
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < GC * D; c += blockDim.x) {
-        const int g = c / D, d = c % D;
-        float mn = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mn = fmaxf(mn, sm_m[w][g]);
-        const float ms = mn == -INFINITY ? 0.f : mn;
-        float sl = 0.f, so = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(sm_m[w][g] - ms);
-            sl = fmaf(sm_l[w][g], f, sl);
-            so = fmaf(sm_o[w][g][d], f, so);
-        }
-        co[g][d] = so;
-        if (d == 0) cm[g] = mn, cl[g] = sl;
-    }
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (split < ng) {  // heads dealt to the CTAs of the cluster
-        for (int g = split; g < ng; g += nsplit)
-            for (int d = threadIdx.x; d < D; d += blockDim.x) {
-                float mn = -INFINITY;
-                for (int r = 0; r < nsplit; ++r) mn = fmaxf(mn, *cluster.map_shared_rank(&cm[g], r));
-                const float ms = mn == -INFINITY ? 0.f : mn;
-                float sl = 0.f, so = 0.f;
-                for (int r = 0; r < nsplit; ++r) {
-                    const float f = exp2f(*cluster.map_shared_rank(&cm[g], r) - ms);
-                    sl = fmaf(*cluster.map_shared_rank(&cl[g], r), f, sl);
-                    so = fmaf(*cluster.map_shared_rank(&co[g][d], r), f, so);
-                }
-                out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
-            }
-    }
-    cluster.sync();
+    join<E, D, GC>(part, joined, out, split, nsplit, ng);
 }
 
-template <typename E, int D, int GC>
-cudaError_t impl(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
+// One step of 16 heads x 8 keys (or 8 channels): D += A B, bf16 operands.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
 {
-    const int G = a.Hq / a.Hk, nchunk = (G + GC - 1) / GC;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pair_bf16(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16 *p)
+{
+    uint4 v;  // (not through the read-only path: another CTA of the cluster may just have put the new token there)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+constexpr int kHeads = 16;  // query heads of a CTA (rows of the matrix instruction)
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
+{
+    using E = __nv_bfloat16;
+    constexpr int NC = D / 32;  // 16-byte chunks of a row per lane
+    __shared__ Partials<kHeads, D> part;
+    __shared__ Joined<kHeads, D> joined;
+    const int split = blockIdx.x, hk = blockIdx.y / nchunk, chunk = blockIdx.y % nchunk, b = blockIdx.z;
+    const int G = a.Hq / a.Hk, g0 = chunk * kHeads, ng = min(kHeads, G - g0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    E *out = static_cast<E *>(a.o) + ((long long)b * a.Hq + hk * G + g0) * D;
+    const int P = a.pos[b];
+    if (P < 0) {  // no sequence in this row
+        if (split == 0)
+            for (int i = threadIdx.x; i < ng * D; i += blockDim.x) out[i] = from_f32<E>(0.f);
+        return;
+    }
+    const E *kn = static_cast<const E *>(a.k) + b * a.ks[0] + hk * a.ks[1];
+    const E *vn = static_cast<const E *>(a.v) + b * a.vs[0] + hk * a.vs[1];
+    if (split == 0 && chunk == 0) put_new_token<E>(a, b, hk, P, kn, vn);
+    const Visible vis(P, a.window, a.sinks, a.slots);
+    const long long cache0 = ((long long)b * a.slots * a.Hk + hk) * D, cstep = (long long)a.Hk * D;
+    const E *kc = static_cast<const E *>(a.kc) + cache0, *vc = static_cast<const E *>(a.vc) + cache0;
+
+    // query heads gr and gr + 8, absent heads as zeros
+    uint4 q[2][NC];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            q[r][j] = gr + 8 * r < ng
+                          ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.q) + b * a.qs[0] +
+                                                             (long long)(hk * G + g0 + gr + 8 * r) * a.qs[1] + (j * 4 + c) * 8)
+                          : make_uint4(0, 0, 0, 0);
+
+    const int per = (vis.n + nsplit - 1) / nsplit;
+    const int t0 = split * per, t1 = min(vis.n, t0 + per);
+    // rows behind the run read its last position again; their scores are masked
+    auto row = [&](const E *fresh, const E *cache, int t) {
+        const int p = vis.position(t < t1 ? t : t1 - 1);
+        return p == P ? fresh : cache + vis.slot(p) * cstep;
+    };
+    uint4 kf[2][NC], vf[4][D / 64];
+    auto load_keys = [&](int t) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const E *p = row(kn, kc, t + gr + 8 * r) + c * 8;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) kf[r][j] = load_stream(p + j * 32);
+        }
+    };
+    auto load_values = [&](int t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const E *p = row(vn, vc, t + 2 * c + (r & 1) + (r >> 1) * 8) + gr * 8;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) vf[r][j] = load_stream(p + j * 64);
+        }
+    };
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
+    const float sc = a.scale * kLog2E;
+    int t = t0 + warp * 16;
+    if (t < t1) {
+        load_keys(t);
+        load_values(t);
+    }
+    for (; t < t1; t += kWarps * 16) {
+        float s[2][4] = {};
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                mma_bf16(s[r], q[0][j].x, q[1][j].x, q[0][j].y, q[1][j].y, kf[r][j].x, kf[r][j].y);
+                mma_bf16(s[r], q[0][j].z, q[1][j].z, q[0][j].w, q[1][j].w, kf[r][j].z, kf[r][j].w);
+            }
+        const int tn = t + kWarps * 16;
+        if (tn < t1) load_keys(tn);
+        // s[r][0..1]: head gr, keys 8 r + 2 c + {0, 1}; s[r][2..3]: head gr + 8
+        float mx[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mx[h] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &v = s[r][2 * h + e];
+                    v = t + 8 * r + 2 * c + e < t1 ? v * sc : -INFINITY;
+                    mx[h] = fmaxf(mx[h], v);
+                }
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 2));
+        }
+        // the reference of a head is raised only when it is outgrown by more than 2^8
+        const bool grow0 = mx[0] > m[0] + 8.f, grow1 = mx[1] > m[1] + 8.f;
+        if (__any_sync(~0u, grow0 || grow1)) {
+            const float f0 = grow0 ? exp2f(m[0] - mx[0]) : 1.f, f1 = grow1 ? exp2f(m[1] - mx[1]) : 1.f;
+            if (grow0) m[0] = mx[0];
+            if (grow1) m[1] = mx[1];
+            l[0] *= f0;
+            l[1] *= f1;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                o[n][0] *= f0;
+                o[n][1] *= f0;
+                o[n][2] *= f1;
+                o[n][3] *= f1;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float ms = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &v = s[r][2 * h + e];
+                    v = exp2f(v - ms);
+                    l[h] += v;
+                }
+        }
+        // P rounded to bf16 for the product (the sum keeps the unrounded values)
+        const uint32_t p0 = pair_bf16(s[0][0], s[0][1]), p1 = pair_bf16(s[0][2], s[0][3]);
+        const uint32_t p2 = pair_bf16(s[1][0], s[1][1]), p3 = pair_bf16(s[1][2], s[1][3]);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const uint32_t *w0 = &vf[0][j].x, *w1 = &vf[1][j].x, *w2 = &vf[2][j].x, *w3 = &vf[3][j].x;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const uint32_t sel = n & 1 ? 0x7632 : 0x5410;
+                mma_bf16(o[j * 8 + n], p0, p1, p2, p3, __byte_perm(w0[n / 2], w1[n / 2], sel),
+                         __byte_perm(w2[n / 2], w3[n / 2], sel));
+            }
+        }
+        if (tn < t1) load_values(tn);
+    }
+    // o[j * 8 + n][0..1]: head gr, channels 64 j + 8 (2 c + {0, 1}) + n; [2..3]: head gr + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(~0u, l[h], 1);
+        l[h] += __shfl_xor_sync(~0u, l[h], 2);
+        const int head = gr + 8 * h;
+        if (c == 0) part.m[warp][head] = m[h], part.l[warp][head] = l[h];
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int n = 0; n < 8; n += 4)
+                    *reinterpret_cast<float4 *>(&part.o[warp][head][64 * j + 8 * (2 * c + e) + n]) =
+                        make_float4(o[j * 8 + n][2 * h + e], o[j * 8 + n + 1][2 * h + e], o[j * 8 + n + 2][2 * h + e],
+                                    o[j * 8 + n + 3][2 * h + e]);
+    }
+    join<E, D, kHeads>(part, joined, out, split, nsplit, ng);
+}
+
+// `gc` query heads of a group per CTA.  The visible positions of a row are split over a
+// cluster while there are fewer CTAs than four times what runs at once (a grid of that size
+// leaves at most a fifth of a wave behind) and every warp has two steps or more.
+template <typename Kernel>
+cudaError_t launch(Kernel kern, const SwaDecodeArgs &a, int gc, int num_sms, cudaStream_t stream)
+{
+    const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc;
     if ((long long)a.Hk * nchunk > 65535) return cudaErrorInvalidValue;
     const long long ctas = (long long)a.B * a.Hk * nchunk;
     int nsplit = 1;
-    while (nsplit < 8 && ctas * nsplit < 2LL * num_sms && (a.window + a.sinks) / (nsplit * 2) >= 64) nsplit *= 2;
+    while (nsplit < 8 && ctas * nsplit < kFill * num_sms && (a.window + a.sinks) / (nsplit * 2) >= 2 * 16 * kWarps) nsplit *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);
     cfg.blockDim = dim3(kWarps * 32);
@@ -199,17 +412,17 @@ cudaError_t impl(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
     attr[0].val.clusterDim.x = nsplit;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<E, D, GC>, a, nsplit, nchunk);
+    cfg.numAttrs = nsplit > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a, nsplit, nchunk);
 }
 
-template <typename E, int D>
-cudaError_t by_group(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
+template <int D>
+cudaError_t by_group_f32(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
 {
     const int G = a.Hq / a.Hk;
-    if (G == 1) return impl<E, D, 1>(a, num_sms, stream);
-    if (G == 2) return impl<E, D, 2>(a, num_sms, stream);
-    return impl<E, D, 4>(a, num_sms, stream);
+    if (G == 1) return launch(decode_kernel<float, D, 1>, a, 1, num_sms, stream);
+    if (G == 2) return launch(decode_kernel<float, D, 2>, a, 2, num_sms, stream);
+    return launch(decode_kernel<float, D, 4>, a, 4, num_sms, stream);
 }
 
 }  // namespace
@@ -217,9 +430,9 @@ cudaError_t by_group(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
 cudaError_t launch_swa_decode(const SwaDecodeArgs &a, bool bf16, int num_sms, cudaStream_t stream)
 {
     if (bf16)
-        return a.d == 128 ? by_group<__nv_bfloat16, 128>(a, num_sms, stream)
-                          : by_group<__nv_bfloat16, 64>(a, num_sms, stream);
-    return a.d == 128 ? by_group<float, 128>(a, num_sms, stream) : by_group<float, 64>(a, num_sms, stream);
+        return a.d == 128 ? launch(decode_mma_kernel<128>, a, kHeads, num_sms, stream)
+                          : launch(decode_mma_kernel<64>, a, kHeads, num_sms, stream);
+    return a.d == 128 ? by_group_f32<128>(a, num_sms, stream) : by_group_f32<64>(a, num_sms, stream);
 }
 
 }  // namespace gdn2
