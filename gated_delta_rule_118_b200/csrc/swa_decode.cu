@@ -26,7 +26,7 @@ using namespace swa;
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
-constexpr long long kFill = 8;  // CTAs per SM that the split of the positions aims at
+constexpr long long kFill = 3;  // CTAs per SM that the split of the positions aims at
 
 // Visible positions in order (sinks behind the window, then the window) -> cache slots.
 struct Visible {
@@ -222,6 +222,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with heads 8..15 absent: their half of the result is not kept.
+__device__ __forceinline__ void mma_bf16(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1)
+{
+    [[maybe_unused]] float none0, none1;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
+                 : "+f"(d[0]), "+f"(d[1]), "=f"(none0), "=f"(none1)
+                 : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pair_bf16(float x, float y)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -234,12 +242,13 @@ __device__ __forceinline__ uint4 load_stream(const __nv_bfloat16 *p)
     return v;
 }
 
-constexpr int kHeads = 16;  // query heads of a CTA (rows of the matrix instruction)
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
+// HR x 8 query heads of a CTA: both halves of the matrix instruction's rows, or one (whose
+// registers then let a third CTA onto the SM, and more loads into flight).
+template <int D, int HR>
+__global__ void __launch_bounds__(kWarps * 32, HR == 1 && D == 64 ? 3 : 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
 {
     using E = __nv_bfloat16;
+    constexpr int kHeads = 8 * HR;
     constexpr int NC = D / 32;  // 16-byte chunks of a row per lane
     __shared__ Partials<kHeads, D> part;
     __shared__ Joined<kHeads, D> joined;
@@ -260,10 +269,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDec
     const long long cache0 = ((long long)b * a.slots * a.Hk + hk) * D, cstep = (long long)a.Hk * D;
     const E *kc = static_cast<const E *>(a.kc) + cache0, *vc = static_cast<const E *>(a.vc) + cache0;
 
-    // query heads gr and gr + 8, absent heads as zeros
-    uint4 q[2][NC];
+    // query heads gr (and gr + 8), absent heads as zeros
+    uint4 q[HR][NC];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < HR; ++r)
 #pragma unroll
         for (int j = 0; j < NC; ++j)
             q[r][j] = gr + 8 * r < ng
@@ -295,7 +304,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDec
             for (int j = 0; j < D / 64; ++j) vf[r][j] = load_stream(p + j * 64);
         }
     };
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
+    float m[HR], l[HR] = {}, o[D / 8][2 * HR] = {};
+#pragma unroll
+    for (int h = 0; h < HR; ++h) m[h] = -INFINITY;
     const float sc = a.scale * kLog2E;
     int t = t0 + warp * 16;
     if (t < t1) {
@@ -303,20 +314,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDec
         load_values(t);
     }
     for (; t < t1; t += kWarps * 16) {
-        float s[2][4] = {};
+        float s[2][2 * HR] = {};
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                mma_bf16(s[r], q[0][j].x, q[1][j].x, q[0][j].y, q[1][j].y, kf[r][j].x, kf[r][j].y);
-                mma_bf16(s[r], q[0][j].z, q[1][j].z, q[0][j].w, q[1][j].w, kf[r][j].z, kf[r][j].w);
+                if constexpr (HR == 2) {
+                    mma_bf16(s[r], q[0][j].x, q[1][j].x, q[0][j].y, q[1][j].y, kf[r][j].x, kf[r][j].y);
+                    mma_bf16(s[r], q[0][j].z, q[1][j].z, q[0][j].w, q[1][j].w, kf[r][j].z, kf[r][j].w);
+                } else {
+                    mma_bf16(s[r], q[0][j].x, q[0][j].y, kf[r][j].x, kf[r][j].y);
+                    mma_bf16(s[r], q[0][j].z, q[0][j].w, kf[r][j].z, kf[r][j].w);
+                }
             }
         const int tn = t + kWarps * 16;
         if (tn < t1) load_keys(tn);
         // s[r][0..1]: head gr, keys 8 r + 2 c + {0, 1}; s[r][2..3]: head gr + 8
-        float mx[2];
+        float mx[HR];
+        bool grow = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < HR; ++h) {
             mx[h] = -INFINITY;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -328,25 +345,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDec
                 }
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 2));
+            grow |= mx[h] > m[h] + 8.f;
         }
         // the reference of a head is raised only when it is outgrown by more than 2^8
-        const bool grow0 = mx[0] > m[0] + 8.f, grow1 = mx[1] > m[1] + 8.f;
-        if (__any_sync(~0u, grow0 || grow1)) {
-            const float f0 = grow0 ? exp2f(m[0] - mx[0]) : 1.f, f1 = grow1 ? exp2f(m[1] - mx[1]) : 1.f;
-            if (grow0) m[0] = mx[0];
-            if (grow1) m[1] = mx[1];
-            l[0] *= f0;
-            l[1] *= f1;
+        if (__any_sync(~0u, grow)) {
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                o[n][0] *= f0;
-                o[n][1] *= f0;
-                o[n][2] *= f1;
-                o[n][3] *= f1;
+            for (int h = 0; h < HR; ++h) {
+                const bool up = mx[h] > m[h] + 8.f;
+                const float f = up ? exp2f(m[h] - mx[h]) : 1.f;
+                if (up) m[h] = mx[h];
+                l[h] *= f;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][2 * h] *= f;
+                    o[n][2 * h + 1] *= f;
+                }
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < HR; ++h) {
             const float ms = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -358,23 +375,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_mma_kernel(const SwaDec
                 }
         }
         // P rounded to bf16 for the product (the sum keeps the unrounded values)
-        const uint32_t p0 = pair_bf16(s[0][0], s[0][1]), p1 = pair_bf16(s[0][2], s[0][3]);
-        const uint32_t p2 = pair_bf16(s[1][0], s[1][1]), p3 = pair_bf16(s[1][2], s[1][3]);
+        uint32_t p[2][HR];  // [keys 0..7, 8..15][heads 0..7, 8..15]
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int h = 0; h < HR; ++h) p[r][h] = pair_bf16(s[r][2 * h], s[r][2 * h + 1]);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
             const uint32_t *w0 = &vf[0][j].x, *w1 = &vf[1][j].x, *w2 = &vf[2][j].x, *w3 = &vf[3][j].x;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
                 const uint32_t sel = n & 1 ? 0x7632 : 0x5410;
-                mma_bf16(o[j * 8 + n], p0, p1, p2, p3, __byte_perm(w0[n / 2], w1[n / 2], sel),
-                         __byte_perm(w2[n / 2], w3[n / 2], sel));
+                const uint32_t b0 = __byte_perm(w0[n / 2], w1[n / 2], sel), b1 = __byte_perm(w2[n / 2], w3[n / 2], sel);
+                if constexpr (HR == 2) mma_bf16(o[j * 8 + n], p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
+                else mma_bf16(o[j * 8 + n], p[0][0], p[1][0], b0, b1);
             }
         }
         if (tn < t1) load_values(tn);
     }
     // o[j * 8 + n][0..1]: head gr, channels 64 j + 8 (2 c + {0, 1}) + n; [2..3]: head gr + 8
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < HR; ++h) {
         l[h] += __shfl_xor_sync(~0u, l[h], 1);
         l[h] += __shfl_xor_sync(~0u, l[h], 2);
         const int head = gr + 8 * h;
@@ -429,9 +450,11 @@ cudaError_t by_group_f32(const SwaDecodeArgs &a, int num_sms, cudaStream_t strea
 
 cudaError_t launch_swa_decode(const SwaDecodeArgs &a, bool bf16, int num_sms, cudaStream_t stream)
 {
-    if (bf16)
-        return a.d == 128 ? launch(decode_mma_kernel<128>, a, kHeads, num_sms, stream)
-                          : launch(decode_mma_kernel<64>, a, kHeads, num_sms, stream);
+    if (bf16) {
+        if (a.d == 64 && a.Hq / a.Hk <= 8) return launch(decode_mma_kernel<64, 1>, a, 8, num_sms, stream);
+        return a.d == 128 ? launch(decode_mma_kernel<128, 2>, a, 16, num_sms, stream)
+                          : launch(decode_mma_kernel<64, 2>, a, 16, num_sms, stream);
+    }
     return a.d == 128 ? by_group_f32<128>(a, num_sms, stream) : by_group_f32<64>(a, num_sms, stream);
 }
 
