@@ -10,7 +10,6 @@ native library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 from pathlib import Path
 
 import torch
@@ -276,44 +275,73 @@ def gdn2_decode_tokens(q, k, v, b, w, log_alpha, S, o=None, *, stream=None, chec
 
 
 # ---------------------------------------------------------------- the hybrid block's other operators
-def _on_device(fn):
-    """Runs ``fn`` with the first tensor's device current, on ``stream`` if one is given (outputs are
-    then allocated for that stream too), else on that device's current stream."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if not (isinstance(first, torch.Tensor) and first.is_cuda):
-            raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError(f"{fn.__name__}: stream is on {stream.device}, tensors on {first.device}")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
+_caller = None
+
+
+def _native():
+    """The module that calls libgdn2.so for the functions below (built with it)."""
+    global _caller
+    if _caller is None:
+        L = lib()
+        from . import _call as module
+        names = ("gdn2_swa_fwd", "gdn2_swa_bwd", "gdn2_swa_decode", "gdn2_scan_fwd", "gdn2_scan_bwd", "gdn2_scan_step",
+                 "gdn2_block_norm_fwd", "gdn2_block_norm_bwd")
+        module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        _caller = module
+    return _caller
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_cuda_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_CODE = {torch.float32: GDN2_F32, torch.bfloat16: GDN2_BF16}
+
+
+def _here(first, stream):
+    """The device of ``first`` if a call can be made as it stands (that device current, no stream given), else -1."""
+    d = first.get_device()
+    return d if d >= 0 and stream is None and d == _cuda_device() else -1
+
+
+def _there(fn, stream, first, *args, **kw):
+    """The call with ``first``'s device current, on ``stream`` if one is given (outputs are then
+    allocated for that stream too), else on that device's current stream."""
+    if not first.is_cuda:
+        raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
+    if stream is not None:
+        if stream.device != first.device:
+            raise ValueError(f"{fn.__name__}: stream is on {stream.device}, tensors on {first.device}")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    with torch.cuda.device(first.device):
         return fn(first, *args, **kw)
-    return call
 
 
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _is(t, shape, dtype, dev):
+    return t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
 
 
-def _need(name, t, shape, dtype, device, dense=True):
-    """``t`` is a tensor of this shape, type and device (None passes)."""
-    if t is None:
+def _need(name, t, shape, dtype, dev, rows=False):
+    """``t`` (None passes) is a dense tensor of this shape and type on device ``dev``; with ``rows``
+    only its last axis has to be contiguous.  Raises otherwise."""
+    if t is None or _is(t, shape, dtype, dev):
         return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if dense:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    elif t.numel() and t.stride(-1) != 1:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if not rows:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.numel() and t.stride(-1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
+
+
+def _code(t):
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _p(t):
@@ -321,215 +349,242 @@ def _p(t):
 
 
 def _done(st, check, where):
-    if check and st != GDN2_OK:
+    if st != GDN2_OK and check:
         raise Gdn2Error(st, where)
 
 
 def _strides(q, k, v):
-    """Host array of the strides of all axes but the last; None if all three are dense."""
+    """The strides of all axes but the last; None if all three are dense."""
     if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
         return None
-    st = [*q.stride()[:-1], *k.stride()[:-1], *v.stride()[:-1]]
-    return (ctypes.c_longlong * len(st))(*st)
+    return (*q.stride()[:-1], *k.stride()[:-1], *v.stride()[:-1])
 
 
-def _swa_sizes(q, k, v, lens, window, sinks, scale):
+def _swa_sizes(q, k, v, lens, window, sinks, scale, dev):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,T,Hq,d], k and v [B,Tk,Hk,d]")
     B, T, Hq, d = q.shape
-    Tk, Hk = k.shape[1], k.shape[2]
-    dt, dev = q.dtype, q.device
-    code = _dtype_code(q)
-    _need("q", q, q.shape, dt, dev, dense=False)
-    _need("k", k, (B, Tk, Hk, d), dt, dev, dense=False)
-    _need("v", v, (B, Tk, Hk, d), dt, dev, dense=False)
-    _need("lens", lens, (B,), torch.int32, dev)
+    _, Tk, Hk, _ = k.shape
+    dt, code = q.dtype, _code(q)
+    shape = (B, Tk, Hk, d)
+    _need("q", q, q.shape, dt, dev, rows=True)
+    _need("k", k, shape, dt, dev, rows=True)
+    _need("v", v, shape, dt, dev, rows=True)
+    if lens is not None:
+        _need("lens", lens, (B,), torch.int32, dev)
     scale = d ** -0.5 if scale is None else float(scale)
-    return (B, T, Tk, Hq, Hk, d, int(window), int(sinks), scale, _strides(q, k, v), code, _raw_stream(dev))
+    return B, T, Tk, Hq, Hk, d, int(window), int(sinks), scale, _strides(q, k, v), code, _raw_stream(dev)
 
 
-@_on_device
-def gdn2_swa_fwd(q, k, v, lens=None, o=None, lse=None, *, window, sinks=0, scale=None, want_lse=True, check=True):
+def gdn2_swa_fwd(q, k, v, lens=None, o=None, lse=None, *, window, sinks=0, scale=None, want_lse=True, stream=None,
+                 check=True):
     """Causal attention over a sliding window and ``sinks`` first tokens.  q [B,T,Hq,d], k and v
     [B,Tk,Hk,d] (Tk >= T; the queries are the last T positions), which may be strided views with
     contiguous rows, such as slices of one packed projection; ``lens`` [B] int32 or None; ``scale``
-    defaults to d ** -0.5.  Also takes ``stream``.  Returns (o, lse), lse [B,Hq,T] fp32 or None
-    unless ``want_lse``."""
-    args = _swa_sizes(q, k, v, lens, window, sinks, scale)
+    defaults to d ** -0.5.  Returns (o, lse), lse [B,Hq,T] fp32 or None unless ``want_lse``."""
+    dev = _here(q, stream)
+    if dev < 0:
+        return _there(gdn2_swa_fwd, stream, q, k, v, lens, o, lse, window=window, sinks=sinks, scale=scale,
+                      want_lse=want_lse, check=check)
+    args = _swa_sizes(q, k, v, lens, window, sinks, scale, dev)
     B, T, Hq, d = q.shape
     if o is None:
         o = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device)
     else:
-        _need("o", o, q.shape, q.dtype, q.device)
+        _need("o", o, q.shape, q.dtype, dev)
     if lse is None:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if want_lse else None
     else:
-        _need("lse", lse, (B, Hq, T), torch.float32, q.device)
-    st = lib().gdn2_swa_fwd(_p(q), _p(k), _p(v), _p(lens), _p(o), _p(lse), *args)
+        _need("lse", lse, (B, Hq, T), torch.float32, dev)
+    st = _native().swa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(lens), o.data_ptr(), _p(lse), *args)
     _done(st, check, "gdn2_swa_fwd")
     return o, lse
 
 
-@_on_device
-def gdn2_swa_bwd(q, k, v, o, lse, dO, lens=None, *, window, sinks=0, scale=None, check=True):
+def gdn2_swa_bwd(q, k, v, o, lse, dO, lens=None, *, window, sinks=0, scale=None, stream=None, check=True):
     """Backward of gdn2_swa_fwd from its inputs, its o and lse, and dO [B,T,Hq,d]; returns a dict
-    of dq, dk and dv (dense, in the inputs' dtype).  Also takes ``stream``."""
-    args = _swa_sizes(q, k, v, lens, window, sinks, scale)
+    of dq, dk and dv (dense, in the inputs' dtype)."""
+    dev = _here(q, stream)
+    if dev < 0:
+        return _there(gdn2_swa_bwd, stream, q, k, v, o, lse, dO, lens, window=window, sinks=sinks, scale=scale,
+                      check=check)
+    args = _swa_sizes(q, k, v, lens, window, sinks, scale, dev)
     B, T, Hq, d = q.shape
-    _need("o", o, q.shape, q.dtype, q.device)
-    _need("dO", dO, q.shape, q.dtype, q.device)
-    _need("lse", lse, (B, Hq, T), torch.float32, q.device)
+    _need("o", o, q.shape, q.dtype, dev)
+    _need("dO", dO, q.shape, q.dtype, dev)
+    _need("lse", lse, (B, Hq, T), torch.float32, dev)
     g = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("dq", q), ("dk", k), ("dv", v))}
-    st = lib().gdn2_swa_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(dO), _p(lens), _p(g["dq"]), _p(g["dk"]),
-                            _p(g["dv"]), *args)
+    st = _native().swa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+                           _p(lens), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), *args)
     _done(st, check, "gdn2_swa_bwd")
     return g
 
 
-@_on_device
-def gdn2_swa_decode(q, k, v, k_cache, v_cache, pos, o=None, *, window, sinks=0, scale=None, check=True):
+def gdn2_swa_decode(q, k, v, k_cache, v_cache, pos, o=None, *, window, sinks=0, scale=None, stream=None, check=True):
     """One token per sequence against a ring cache: q [B,Hq,d], new k and v [B,Hk,d] (all three may
     be strided views with contiguous rows), k_cache and v_cache [B,slots,Hk,d] updated in place, pos
     [B] int32 the new token's position (< 0: no sequence in this row).  Position p lives in slot p if
-    p < sinks, else in slot sinks + (p - sinks) % (slots - sinks).  Also takes ``stream``.  Returns o."""
+    p < sinks, else in slot sinks + (p - sinks) % (slots - sinks).  Returns o."""
+    dev = _here(q, stream)
+    if dev < 0:
+        return _there(gdn2_swa_decode, stream, q, k, v, k_cache, v_cache, pos, o, window=window, sinks=sinks,
+                      scale=scale, check=check)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [B,Hq,d], the caches [B,slots,Hk,d]")
     B, Hq, d = q.shape
-    slots, Hk = k_cache.shape[1], k_cache.shape[2]
-    dt, dev = q.dtype, q.device
-    code = _dtype_code(q)
-    _need("q", q, q.shape, dt, dev, dense=False)
-    _need("k", k, (B, Hk, d), dt, dev, dense=False)
-    _need("v", v, (B, Hk, d), dt, dev, dense=False)
+    cache = k_cache.shape
+    _, slots, Hk, _ = cache
+    dt, code = q.dtype, _code(q)
+    row = (B, Hk, d)
+    _need("q", q, q.shape, dt, dev, rows=True)
+    _need("k", k, row, dt, dev, rows=True)
+    _need("v", v, row, dt, dev, rows=True)
     _need("k_cache", k_cache, (B, slots, Hk, d), dt, dev)
-    _need("v_cache", v_cache, (B, slots, Hk, d), dt, dev)
+    _need("v_cache", v_cache, cache, dt, dev)
     _need("pos", pos, (B,), torch.int32, dev)
     if o is None:
-        o = torch.empty((B, Hq, d), dtype=dt, device=dev)
+        o = torch.empty((B, Hq, d), dtype=dt, device=q.device)
     else:
         _need("o", o, q.shape, dt, dev)
-    st = lib().gdn2_swa_decode(_p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(pos), _p(o), B, slots, Hq, Hk, d,
-                               int(window), int(sinks), d ** -0.5 if scale is None else float(scale),
-                               _strides(q, k, v), code, _raw_stream(dev))
+    st = _native().swa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                              pos.data_ptr(), o.data_ptr(), B, slots, Hq, Hk, d, int(window), int(sinks),
+                              d ** -0.5 if scale is None else float(scale), _strides(q, k, v), code, _raw_stream(dev))
     _done(st, check, "gdn2_swa_decode")
     return o
 
 
-@_on_device
-def gdn2_scan_fwd(x, w, log_alpha, h0=None, y=None, h_T=None, *, want_state=True, want_ckpt=False, check=True):
+def gdn2_scan_fwd(x, w, log_alpha, h0=None, y=None, h_T=None, *, want_state=True, want_ckpt=False, stream=None,
+                  check=True):
     """Gated linear recurrence h_t = exp(log_alpha_t) h_{t-1} + w_t x_t per channel: x, w [B,T,C],
-    log_alpha [B,T,C] fp32, h0 [B,C] fp32 or None.  Also takes ``stream``.  Returns (y, h_T), and with
-    ``want_ckpt`` (y, h_T, ckpt), ckpt being what gdn2_scan_bwd needs."""
-    B, T, C = x.shape
-    dev = x.device
-    code = _dtype_code(x)
-    _need("x", x, x.shape, x.dtype, dev)
-    _need("w", w, x.shape, x.dtype, dev)
-    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
+    log_alpha [B,T,C] fp32, h0 [B,C] fp32 or None.  Returns (y, h_T), and with ``want_ckpt``
+    (y, h_T, ckpt), ckpt being what gdn2_scan_bwd needs."""
+    dev = _here(x, stream)
+    if dev < 0:
+        return _there(gdn2_scan_fwd, stream, x, w, log_alpha, h0, y, h_T, want_state=want_state, want_ckpt=want_ckpt,
+                      check=check)
+    shape = x.shape
+    B, T, C = shape
+    dt, code = x.dtype, _code(x)
+    _need("x", x, shape, dt, dev)
+    _need("w", w, shape, dt, dev)
+    _need("log_alpha", log_alpha, shape, torch.float32, dev)
     _need("h0", h0, (B, C), torch.float32, dev)
-    _need("y", y, x.shape, x.dtype, dev)
+    _need("y", y, shape, dt, dev)
     _need("h_T", h_T, (B, C), torch.float32, dev)
     if y is None:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        y = torch.empty_like(x)
     if h_T is None and want_state:
-        h_T = torch.empty((B, C), dtype=torch.float32, device=dev)
+        h_T = torch.empty((B, C), dtype=torch.float32, device=x.device)
     ckpt = None
     if want_ckpt:
-        ckpt = torch.empty((B, -(-T // GDN2_SCAN_BLOCK), C), dtype=torch.float32, device=dev)
-    st = lib().gdn2_scan_fwd(_p(x), _p(w), _p(log_alpha), _p(h0), _p(y), _p(h_T), _p(ckpt), B, T, C, code,
-                             _raw_stream(dev))
+        ckpt = torch.empty((B, -(-T // GDN2_SCAN_BLOCK), C), dtype=torch.float32, device=x.device)
+    st = _native().scan_fwd(x.data_ptr(), w.data_ptr(), log_alpha.data_ptr(), _p(h0), y.data_ptr(), _p(h_T), _p(ckpt),
+                            B, T, C, code, _raw_stream(dev))
     _done(st, check, "gdn2_scan_fwd")
     return (y, h_T, ckpt) if want_ckpt else (y, h_T)
 
 
-@_on_device
-def gdn2_scan_bwd(x, w, log_alpha, ckpt, dy, dh_T=None, *, want_dh0=True, check=True):
-    """Backward of gdn2_scan_fwd: its inputs and ckpt, dy [B,T,C] and dh_T [B,C] fp32 or None.  Also
-    takes ``stream``.  Returns a dict of dx, dw (inputs' dtype), dlog_alpha and dh0 (fp32; dh0 None
-    unless ``want_dh0``)."""
-    B, T, C = x.shape
-    dev = x.device
-    code = _dtype_code(x)
-    _need("x", x, x.shape, x.dtype, dev)
-    _need("w", w, x.shape, x.dtype, dev)
-    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
+def gdn2_scan_bwd(x, w, log_alpha, ckpt, dy, dh_T=None, *, want_dh0=True, stream=None, check=True):
+    """Backward of gdn2_scan_fwd: its inputs and ckpt, dy [B,T,C] and dh_T [B,C] fp32 or None.
+    Returns a dict of dx, dw (inputs' dtype), dlog_alpha and dh0 (fp32; dh0 None unless ``want_dh0``)."""
+    dev = _here(x, stream)
+    if dev < 0:
+        return _there(gdn2_scan_bwd, stream, x, w, log_alpha, ckpt, dy, dh_T, want_dh0=want_dh0, check=check)
+    shape = x.shape
+    B, T, C = shape
+    dt, code = x.dtype, _code(x)
+    _need("x", x, shape, dt, dev)
+    _need("w", w, shape, dt, dev)
+    _need("log_alpha", log_alpha, shape, torch.float32, dev)
     _need("ckpt", ckpt, (B, -(-T // GDN2_SCAN_BLOCK), C), torch.float32, dev)
-    _need("dy", dy, x.shape, x.dtype, dev)
+    _need("dy", dy, shape, dt, dev)
     _need("dh_T", dh_T, (B, C), torch.float32, dev)
-    g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
-         "dw": torch.empty((B, T, C), dtype=x.dtype, device=dev),
-         "dlog_alpha": torch.empty((B, T, C), dtype=torch.float32, device=dev),
-         "dh0": torch.empty((B, C), dtype=torch.float32, device=dev) if want_dh0 else None}
-    st = lib().gdn2_scan_bwd(_p(x), _p(w), _p(log_alpha), _p(ckpt), _p(dy), _p(dh_T), _p(g["dx"]), _p(g["dw"]),
-                             _p(g["dlog_alpha"]), _p(g["dh0"]), B, T, C, code, _raw_stream(dev))
+    g = {"dx": torch.empty_like(x), "dw": torch.empty_like(x), "dlog_alpha": torch.empty_like(log_alpha),
+         "dh0": torch.empty((B, C), dtype=torch.float32, device=x.device) if want_dh0 else None}
+    st = _native().scan_bwd(x.data_ptr(), w.data_ptr(), log_alpha.data_ptr(), ckpt.data_ptr(), dy.data_ptr(), _p(dh_T),
+                            g["dx"].data_ptr(), g["dw"].data_ptr(), g["dlog_alpha"].data_ptr(), _p(g["dh0"]),
+                            B, T, C, code, _raw_stream(dev))
     _done(st, check, "gdn2_scan_bwd")
     return g
 
 
-@_on_device
-def gdn2_scan_step(x, w, log_alpha, h, y=None, *, check=True):
+def gdn2_scan_step(x, w, log_alpha, h, y=None, *, stream=None, check=True):
     """One token of the recurrence: x, w [B,C], log_alpha and h [B,C] fp32, h updated in place.
-    Also takes ``stream``.  Returns y."""
-    B, C = x.shape
-    dev = x.device
-    code = _dtype_code(x)
-    _need("x", x, x.shape, x.dtype, dev)
-    _need("w", w, x.shape, x.dtype, dev)
-    _need("log_alpha", log_alpha, x.shape, torch.float32, dev)
-    _need("h", h, x.shape, torch.float32, dev)
+    Returns y."""
+    dev = _here(x, stream)
+    if dev < 0:
+        return _there(gdn2_scan_step, stream, x, w, log_alpha, h, y, check=check)
+    shape = x.shape
+    B, C = shape
+    dt, code = x.dtype, _code(x)
+    _need("x", x, shape, dt, dev)
+    _need("w", w, shape, dt, dev)
+    _need("log_alpha", log_alpha, shape, torch.float32, dev)
+    _need("h", h, shape, torch.float32, dev)
     if y is None:
-        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        y = torch.empty_like(x)
     else:
-        _need("y", y, x.shape, x.dtype, dev)
-    st = lib().gdn2_scan_step(_p(x), _p(w), _p(log_alpha), _p(h), _p(y), B, C, code, _raw_stream(dev))
+        _need("y", y, shape, dt, dev)
+    st = _native().scan_step(x.data_ptr(), w.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), y.data_ptr(), B, C, code,
+                             _raw_stream(dev))
     _done(st, check, "gdn2_scan_step")
     return y
 
 
-def _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre):
-    D, dev = r.shape[-1], r.device
-    _need("r", r, r.shape, r.dtype, dev)
-    _need("y", y, r.shape, r.dtype, dev)
-    _need("g_logit", g_logit, r.shape, r.dtype, dev)
-    for name, t in (("w_post", w_post), ("res_scale", res_scale), ("w_pre", w_pre)):
-        _need(name, t, (D,), torch.float32, dev)
-    return r.numel() // D if D else 0, D, _dtype_code(r)
+def _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre, dev):
+    shape = r.shape
+    D, dt, code = shape[-1], r.dtype, _code(r)
+    _need("r", r, shape, dt, dev)
+    _need("y", y, shape, dt, dev)
+    _need("g_logit", g_logit, shape, dt, dev)
+    _need("w_post", w_post, (D,), torch.float32, dev)
+    _need("res_scale", res_scale, (D,), torch.float32, dev)
+    _need("w_pre", w_pre, (D,), torch.float32, dev)
+    return r.numel() // D if D else 0, D, code
 
 
-@_on_device
-def gdn2_block_norm_fwd(r, y, g_logit, w_post, res_scale, w_pre, eps=1e-6, r_out=None, x_out=None, *, check=True):
+def gdn2_block_norm_fwd(r, y, g_logit, w_post, res_scale, w_pre, eps=1e-6, r_out=None, x_out=None, *, stream=None,
+                        check=True):
     """The norms around a block: r_out = r + res_scale * sigmoid(g_logit) * RMSNorm(y) * w_post and
     x_out = RMSNorm(r_out) * w_pre, over the last axis (r, y, g_logit of one shape; g_logit None: no
-    gate; the three vectors fp32).  r_out may be r.  Also takes ``stream``.  Returns (r_out, x_out)."""
-    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre)
-    _need("r_out", r_out, r.shape, r.dtype, r.device)
-    _need("x_out", x_out, r.shape, r.dtype, r.device)
+    gate; the three vectors fp32).  r_out may be r.  Returns (r_out, x_out)."""
+    dev = _here(r, stream)
+    if dev < 0:
+        return _there(gdn2_block_norm_fwd, stream, r, y, g_logit, w_post, res_scale, w_pre, eps, r_out, x_out,
+                      check=check)
+    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre, dev)
+    _need("r_out", r_out, r.shape, r.dtype, dev)
+    _need("x_out", x_out, r.shape, r.dtype, dev)
     if r_out is None:
-        r_out = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+        r_out = torch.empty_like(r)
     if x_out is None:
-        x_out = torch.empty(r.shape, dtype=r.dtype, device=r.device)
-    st = lib().gdn2_block_norm_fwd(_p(r), _p(y), _p(g_logit), _p(w_post), _p(res_scale), _p(w_pre), float(eps),
-                                   _p(r_out), _p(x_out), N, D, code, _raw_stream(r.device))
+        x_out = torch.empty_like(r)
+    st = _native().block_norm_fwd(r.data_ptr(), y.data_ptr(), _p(g_logit), w_post.data_ptr(), res_scale.data_ptr(),
+                                  w_pre.data_ptr(), eps, r_out.data_ptr(), x_out.data_ptr(), N, D, code,
+                                  _raw_stream(dev))
     _done(st, check, "gdn2_block_norm_fwd")
     return r_out, x_out
 
 
-@_on_device
-def gdn2_block_norm_bwd(r, y, g_logit, w_post, res_scale, w_pre, dr_out, dx_out, eps=1e-6, *, check=True):
-    """Backward of gdn2_block_norm_fwd from its inputs and the gradients of r_out and x_out.  Also
-    takes ``stream``.  Returns a dict of dr, dy, dg_logit (inputs' dtype; dg_logit None without a
-    gate), dw_post, dres_scale and dw_pre (fp32)."""
-    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre)
-    _need("dr_out", dr_out, r.shape, r.dtype, r.device)
-    _need("dx_out", dx_out, r.shape, r.dtype, r.device)
-    like = dict(dtype=r.dtype, device=r.device)
-    g = {"dr": torch.empty(r.shape, **like), "dy": torch.empty(r.shape, **like),
-         "dg_logit": None if g_logit is None else torch.empty(r.shape, **like)}
-    g.update({n: torch.empty((D,), dtype=torch.float32, device=r.device) for n in ("dw_post", "dres_scale", "dw_pre")})
-    st = lib().gdn2_block_norm_bwd(_p(r), _p(y), _p(g_logit), _p(w_post), _p(res_scale), _p(w_pre), float(eps),
-                                   _p(dr_out), _p(dx_out), _p(g["dr"]), _p(g["dy"]), _p(g["dg_logit"]),
-                                   _p(g["dw_post"]), _p(g["dres_scale"]), _p(g["dw_pre"]), N, D, code,
-                                   _raw_stream(r.device))
+def gdn2_block_norm_bwd(r, y, g_logit, w_post, res_scale, w_pre, dr_out, dx_out, eps=1e-6, *, stream=None,
+                        check=True):
+    """Backward of gdn2_block_norm_fwd from its inputs and the gradients of r_out and x_out.  Returns
+    a dict of dr, dy, dg_logit (inputs' dtype; dg_logit None without a gate), dw_post, dres_scale and
+    dw_pre (fp32)."""
+    dev = _here(r, stream)
+    if dev < 0:
+        return _there(gdn2_block_norm_bwd, stream, r, y, g_logit, w_post, res_scale, w_pre, dr_out, dx_out, eps,
+                      check=check)
+    N, D, code = _norm_inputs(r, y, g_logit, w_post, res_scale, w_pre, dev)
+    _need("dr_out", dr_out, r.shape, r.dtype, dev)
+    _need("dx_out", dx_out, r.shape, r.dtype, dev)
+    g = {"dr": torch.empty_like(r), "dy": torch.empty_like(r),
+         "dg_logit": None if g_logit is None else torch.empty_like(r), "dw_post": torch.empty_like(w_post),
+         "dres_scale": torch.empty_like(w_post), "dw_pre": torch.empty_like(w_post)}
+    st = _native().block_norm_bwd(r.data_ptr(), y.data_ptr(), _p(g_logit), w_post.data_ptr(), res_scale.data_ptr(),
+                                  w_pre.data_ptr(), eps, dr_out.data_ptr(), dx_out.data_ptr(), g["dr"].data_ptr(),
+                                  g["dy"].data_ptr(), _p(g["dg_logit"]), g["dw_post"].data_ptr(),
+                                  g["dres_scale"].data_ptr(), g["dw_pre"].data_ptr(), N, D, code, _raw_stream(dev))
     _done(st, check, "gdn2_block_norm_bwd")
     return g
 

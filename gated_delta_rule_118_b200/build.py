@@ -1,9 +1,11 @@
-"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a, and the Python
+module that calls it (_call.so) with the host compiler."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -11,6 +13,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libgdn2.so"
+CALLER = PKG / "_call.so"
 OBJDIR = PKG / "_build"
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -28,18 +31,18 @@ def sources() -> list[Path]:
 
 
 def _deps() -> list[Path]:
-    return sources() + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h"))
+    return sources() + sorted(CSRC.glob("*.c")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h"))
 
 
 def is_stale() -> bool:
-    if not LIBRARY.exists():
+    if not LIBRARY.exists() or not CALLER.exists():
         return True
-    t = LIBRARY.stat().st_mtime
+    t = min(LIBRARY.stat().st_mtime, CALLER.stat().st_mtime)
     return any(p.stat().st_mtime > t for p in _deps())
 
 
 def build_library(force: bool = False, verbose: bool = False) -> Path:
-    """Compile every csrc/*.cu to an object and link them into libgdn2.so."""
+    """Compile every csrc/*.cu to an object and link them into libgdn2.so; compile _call.so."""
     if not force and not is_stale():
         return LIBRARY
     OBJDIR.mkdir(exist_ok=True)
@@ -62,7 +65,14 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    caller = CALLER.with_suffix(".so.tmp")
+    host = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall", "-Wno-unused-parameter",
+            f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", str(CSRC / "binding.c"), "-o", str(caller)]
+    r = subprocess.run(host, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{host[0]} failed on binding.c:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
+    os.replace(caller, CALLER)
     (OBJDIR / "ptxas.log").write_text("\n".join(logs))
     if verbose:
         print("\n".join(logs))
