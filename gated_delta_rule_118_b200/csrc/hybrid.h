@@ -25,10 +25,11 @@ struct SwaArgs {
 };
 cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t stream);     // fp32
 cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t stream);  // bf16
-cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t stream);     // fp32
-// bf16; `part`: swa_bwd_tc_partial_floats(...) of workspace (partial sums of the sinks' gradients)
+// Backward; `part`: ..._partial_floats(...) of workspace for partial sums of dk and dv.
+size_t swa_bwd_simt_partial_floats(const SwaArgs &a, int num_sms);
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream);  // fp32
 size_t swa_bwd_tc_partial_floats(const SwaArgs &a, int num_sms);
-cudaError_t launch_swa_bwd_tc(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream);
+cudaError_t launch_swa_bwd_tc(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream);    // bf16
 cudaError_t launch_swa_delta(const SwaArgs &a, bool bf16, cudaStream_t stream);
 
 struct SwaDecodeArgs {

@@ -133,11 +133,12 @@ extern "C" gdn2_status gdn2_swa_bwd(const void *q, const void *k, const void *v,
     void *ws = nullptr;
     const bool tc = dtype == GDN2_BF16;
     const size_t rows = ((size_t)B * Hq * T + 3) / 4 * 4;  // (the partial sums behind delta stay 16-byte aligned)
-    const size_t part = tc ? swa_bwd_tc_partial_floats(a, sms) : 0;
+    const size_t part = tc ? swa_bwd_tc_partial_floats(a, sms) : swa_bwd_simt_partial_floats(a, sms);
     if (cudaMallocFromPoolAsync(&ws, sizeof(float) * (rows + part), pool, s) != cudaSuccess) return GDN2_ERR_CUDA;
     a.delta = static_cast<float *>(ws);
     cudaError_t e = launch_swa_delta(a, tc, s);
-    if (e == cudaSuccess) e = tc ? launch_swa_bwd_tc(a, a.delta + rows, sms, s) : launch_swa_bwd_simt(a, s);
+    if (e == cudaSuccess)
+        e = tc ? launch_swa_bwd_tc(a, a.delta + rows, sms, s) : launch_swa_bwd_simt(a, a.delta + rows, sms, s);
     const cudaError_t fe = cudaFreeAsync(ws, s);
     return from_cuda(e == cudaSuccess ? fe : e);
 }

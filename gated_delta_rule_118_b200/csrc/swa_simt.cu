@@ -257,16 +257,18 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
         if (bad[r >> 5] >> (r & 31) & 1) row_dq<E, D>(a, b, h, i0 + r);
 }
 
-// dk and dv of 64 keys, query tiles of 32 rows over all heads of the group.
+// dk and dv of 64 keys, query tiles of 32 rows over all heads of the group.  With nsplit
+// > 1 the (head, query tile) pairs of a key tile are dealt to nsplit CTAs, whose sums
+// another kernel adds in order: part [nsplit][B][Hk][Tk][2][D].
 template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
+__global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a, int nsplit, float *part)
 {
     constexpr int LD = D + 4, PS = 68;
     extern __shared__ float sm[];
     float *Ks = sm, *Vs = Ks + 64 * LD, *Qs = Vs + 64 * LD, *Gs = Qs + 32 * LD, *Ps = Gs + 32 * LD;
     __shared__ unsigned bad[2];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const int j0 = blockIdx.x * 64, hk = blockIdx.y, b = blockIdx.z;
+    const int j0 = (int)(blockIdx.x / nsplit) * 64, split = blockIdx.x % nsplit, hk = blockIdx.y, b = blockIdx.z;
     const int n = seq_len(a, b), off = a.Tk - a.T, G = a.Hq / a.Hk;
     if (tid < 2) bad[tid] = 0;
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
@@ -275,10 +277,13 @@ __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
     const int i_lo = max(j0 - off, 0);
     const long long far = (long long)min(j0 + 64, a.Tk) - 1 + a.window - off;  // first row behind every window
     const int i_hi = (j0 < a.sinks || far > n) ? n : (int)far;
-    for (int h = hk * G; h < hk * G + G; ++h) {
+    const int nq = i_hi > i_lo ? (i_hi - i_lo + 31) / 32 : 0;
+    const long long all = (long long)G * nq, per = (all + nsplit - 1) / nsplit;
+    for (long long it = split * per; it < min(all, (split + 1) * per); ++it) {
+        const int h = hk * G + (int)(it / nq), i0 = i_lo + (int)(it % nq) * 32;
         const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D);
         const long long lrow = ((long long)b * a.Hq + h) * a.T;
-        for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+        {
             __syncthreads();
             load_rows<E, D, 32>(Qs, q, i0, n);
             load_rows<E, D, 32>(Gs, g, i0, n);
@@ -310,6 +315,17 @@ __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
         }
     }
     __syncthreads();
+    if (nsplit > 1) {
+        float *out = part + ((((long long)split * a.B + b) * a.Hk + hk) * a.Tk) * 2 * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + ty * 4 + i;
+            if (j >= a.Tk) continue;
+            store_cols<float, D>(out + (long long)j * 2 * D, dk[i], a.scale, tx);
+            store_cols<float, D>(out + (long long)j * 2 * D + D, dv[i], 1.f, tx);
+        }
+        return;
+    }
     E *ok = const_cast<E *>(dense_rows<E>(a.dk, b, hk, a.Tk, a.Hk, D)[0]);
     E *ov = const_cast<E *>(dense_rows<E>(a.dv, b, hk, a.Tk, a.Hk, D)[0]);
     const long long st = (long long)a.Hk * D;
@@ -324,6 +340,40 @@ __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a)
     __syncthreads();
     for (int r = tid >> 5; r < 64; r += kThreads / 32)
         if (bad[r >> 5] >> (r & 31) & 1) row_dkdv<E, D>(a, b, hk, j0 + r);
+}
+
+// The segments' sums added in order, one warp a key.
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) dkdv_sum_kernel(const SwaArgs a, int nsplit, const float *part)
+{
+    const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), rows = (long long)a.B * a.Hk * a.Tk;
+    if (row >= rows) return;  // row = (b, hk, j)
+    const int lane = threadIdx.x & 31, j = (int)(row % a.Tk), hk = (int)(row / a.Tk % a.Hk), b = (int)(row / a.Tk / a.Hk);
+    float v[2 * D / 32] = {};
+    for (int s = 0; s < nsplit; ++s)
+#pragma unroll
+        for (int u = 0; u < 2 * D / 32; ++u) v[u] += part[(s * rows + row) * 2 * D + lane + 32 * u];
+    const long long at = (((long long)b * a.Tk + j) * a.Hk + hk) * D;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        bad |= !isfinite(v[u]) || !isfinite(v[D / 32 + u]);
+        static_cast<E *>(a.dk)[at + lane + 32 * u] = from_f32<E>(v[u]);
+        static_cast<E *>(a.dv)[at + lane + 32 * u] = from_f32<E>(v[D / 32 + u]);
+    }
+    if (__any_sync(~0u, bad)) row_dkdv<E, D>(a, b, hk, j);
+}
+
+// How many CTAs share a key tile: as many as bring the grid to twice the SMs, while each
+// keeps four query tiles or more.
+int kv_split(const SwaArgs &a, int num_sms)
+{
+    const long long ctas = (long long)((a.Tk + 63) / 64) * a.Hk * a.B;
+    const long long seen = a.sinks > 0 ? a.T : (a.window + 63LL < a.T ? a.window + 63LL : a.T);
+    const long long tiles = (seen + 31) / 32 * (a.Hq / a.Hk);
+    int n = 1;
+    while (n < 8 && ctas * n < 2LL * num_sms && tiles / (n * 2) >= 4) n *= 2;
+    return n;
 }
 
 // delta = dO . o of every row that holds a token, one warp per row.
@@ -354,7 +404,7 @@ cudaError_t fwd_impl(const SwaArgs &a, cudaStream_t stream)
 }
 
 template <typename E, int D>
-cudaError_t bwd_impl(const SwaArgs &a, cudaStream_t stream)
+cudaError_t bwd_impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
 {
     constexpr int dq_bytes = sizeof(float) * (192 * (D + 4) + 64 * 36), kv_bytes = sizeof(float) * (192 * (D + 4) + 32 * 68);
     cudaError_t e = cudaFuncSetAttribute(dq_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_bytes);
@@ -364,7 +414,12 @@ cudaError_t bwd_impl(const SwaArgs &a, cudaStream_t stream)
     dq_kernel<E, D><<<dim3((a.T + 63) / 64, a.Hq, a.B), kThreads, dq_bytes, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    dkdv_kernel<E, D><<<dim3((a.Tk + 63) / 64, a.Hk, a.B), kThreads, kv_bytes, stream>>>(a);
+    const int nsplit = kv_split(a, num_sms);
+    dkdv_kernel<E, D><<<dim3((a.Tk + 63) / 64 * nsplit, a.Hk, a.B), kThreads, kv_bytes, stream>>>(a, nsplit, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || nsplit == 1) return e;
+    const long long keys = (long long)a.B * a.Hk * a.Tk;
+    dkdv_sum_kernel<E, D><<<(unsigned)((keys + 7) / 8), kThreads, 0, stream>>>(a, nsplit, part);
     return cudaGetLastError();
 }
 
@@ -384,9 +439,15 @@ cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t stream)
     return a.d == 128 ? fwd_impl<float, 128>(a, stream) : fwd_impl<float, 64>(a, stream);
 }
 
-cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t stream)
+size_t swa_bwd_simt_partial_floats(const SwaArgs &a, int num_sms)
 {
-    return a.d == 128 ? bwd_impl<float, 128>(a, stream) : bwd_impl<float, 64>(a, stream);
+    const int n = kv_split(a, num_sms);
+    return n > 1 ? (size_t)n * a.B * a.Hk * a.Tk * 2 * a.d : 0;
+}
+
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
+{
+    return a.d == 128 ? bwd_impl<float, 128>(a, part, num_sms, stream) : bwd_impl<float, 64>(a, part, num_sms, stream);
 }
 
 cudaError_t launch_swa_delta(const SwaArgs &a, bool bf16, cudaStream_t stream)
