@@ -25,8 +25,6 @@ namespace {
 using namespace swa;
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 4;
-constexpr long long kFill = 3;  // CTAs per SM that the split of the positions aims at
 
 // Visible positions in order (sinks behind the window, then the window) -> cache slots.
 struct Visible {
@@ -62,30 +60,48 @@ __device__ __forceinline__ void put_new_token(const SwaDecodeArgs &a, int b, int
 }
 
 // The warps' partial results of a CTA, and the CTA's.
-template <int GC, int D>
+template <int NW, int GC, int D>
 struct Partials {
-    float m[kWarps][GC], l[kWarps][GC];
-    alignas(16) float o[kWarps][GC][D];
+    float m[NW][GC], l[NW][GC];
+    alignas(16) float o[NW][GC][D];
 };
+// What the CTAs of a cluster send to the one that joins a head: slot (CTA, head).
+constexpr int kMaxSplit = 8;
 template <int GC, int D>
 struct Joined {
-    float m[GC], l[GC], o[GC][D];
+    static constexpr int HEADS = (GC + 1) / 2;  // of one joining CTA, when there are two or more
+    float m[kMaxSplit][HEADS], l[kMaxSplit][HEADS], o[kMaxSplit][HEADS][D];
 };
 
-// Joins the warps, then the CTAs of the cluster, and writes the heads [0, ng).
-template <typename E, int D, int GC>
-__device__ __forceinline__ void join(const Partials<GC, D> &part, Joined<GC, D> &mine, E *out, int split, int nsplit, int ng)
+// A barrier of the cluster in two halves: every CTA has started (arrived) before another
+// stores into its shared memory (waited), without holding up the work between.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+template <int NW, int GC, int D>
+struct DecodeShared {
+    Partials<NW, GC, D> part;
+    Joined<GC, D> joined;
+};
+
+// Joins the warps, then the CTAs of the cluster, and writes the heads [0, ng).  Head g is
+// joined by CTA g % nsplit: the others store their part into its shared memory (one way,
+// where reading would be a round trip per value).
+template <typename E, int D, int NW, int GC>
+__device__ __forceinline__ void join(const Partials<NW, GC, D> &part, Joined<GC, D> &mine, E *out, int split, int nsplit, int ng)
 {
+    cg::cluster_group cluster = cg::this_cluster();
     __syncthreads();
+    cluster_wait();
     for (int i = threadIdx.x; i < ng * D; i += blockDim.x) {
         const int g = i / D, d = i % D;
         float mn = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mn = fmaxf(mn, part.m[w][g]);
+        for (int w = 0; w < NW; ++w) mn = fmaxf(mn, part.m[w][g]);
         const float ms = mn == -INFINITY ? 0.f : mn;
         float sl = 0.f, so = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = exp2f(part.m[w][g] - ms);
             sl = fmaf(part.l[w][g], f, sl);
             so = fmaf(part.o[w][g][d], f, so);
@@ -93,43 +109,50 @@ __device__ __forceinline__ void join(const Partials<GC, D> &part, Joined<GC, D> 
         if (nsplit == 1) {
             out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
         } else {
-            mine.o[g][d] = so;
-            if (d == 0) mine.m[g] = mn, mine.l[g] = sl;
+            const int to = g % nsplit, at = g / nsplit;
+            *cluster.map_shared_rank(&mine.o[split][at][d], to) = so;
+            if (d == 0) {
+                *cluster.map_shared_rank(&mine.m[split][at], to) = mn;
+                *cluster.map_shared_rank(&mine.l[split][at], to) = sl;
+            }
         }
     }
     if (nsplit == 1) return;
-    cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    for (int g = split; g < ng; g += nsplit)  // heads dealt to the CTAs of the cluster
-        for (int d = threadIdx.x; d < D; d += blockDim.x) {
-            float mn = -INFINITY;
-            for (int r = 0; r < nsplit; ++r) mn = fmaxf(mn, *cluster.map_shared_rank(&mine.m[g], r));
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            float sl = 0.f, so = 0.f;
-            for (int r = 0; r < nsplit; ++r) {
-                const float f = exp2f(*cluster.map_shared_rank(&mine.m[g], r) - ms);
-                sl = fmaf(*cluster.map_shared_rank(&mine.l[g], r), f, sl);
-                so = fmaf(*cluster.map_shared_rank(&mine.o[g][d], r), f, so);
-            }
-            out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
+    for (int i = threadIdx.x; i < ng * D; i += blockDim.x) {
+        const int at = i / D, d = i % D, g = at * nsplit + split;
+        if (g >= ng) break;
+        float mn = -INFINITY;
+        for (int r = 0; r < nsplit; ++r) mn = fmaxf(mn, mine.m[r][at]);
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        float sl = 0.f, so = 0.f;
+        for (int r = 0; r < nsplit; ++r) {
+            const float f = exp2f(mine.m[r][at] - ms);
+            sl = fmaf(mine.l[r][at], f, sl);
+            so = fmaf(mine.o[r][at][d], f, so);
         }
-    cluster.sync();
+        out[g * D + d] = from_f32<E>(sl == 0.f ? 0.f : so / sl);
+    }
 }
 
 // GC query heads of the group per CTA; lanes hold 4 channels each of D / 4 lanes per key.
 template <typename E, int D, int GC>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
+__global__ void __launch_bounds__(4 * 32) decode_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
 {
     constexpr int LPR = D / 4, KPW = 32 / LPR;  // lanes per key, keys per warp step
-    constexpr int U = 4;                        // steps in flight
-    __shared__ Partials<GC, D> part;
-    __shared__ Joined<GC, D> joined;
+    constexpr int U = 4, NW = 4;                // steps in flight, warps
+    using Shared = DecodeShared<NW, GC, D>;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    auto &part = reinterpret_cast<Shared *>(dyn)->part;
+    auto &joined = reinterpret_cast<Shared *>(dyn)->joined;
     const int split = blockIdx.x, hk = blockIdx.y / nchunk, chunk = blockIdx.y % nchunk, b = blockIdx.z;
     const int G = a.Hq / a.Hk, g0 = chunk * GC, ng = min(GC, G - g0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, x = lane % LPR * 4;
     E *out = static_cast<E *>(a.o) + ((long long)b * a.Hq + hk * G + g0) * D;
+    cluster_arrive();
     const int P = a.pos[b];
     if (P < 0) {  // no sequence in this row
+        cluster_wait();
         if (split == 0)
             for (int c = threadIdx.x; c < ng * D; c += blockDim.x) out[c] = from_f32<E>(0.f);
         return;
@@ -153,7 +176,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs
     }
     const int per = (vis.n + nsplit - 1) / nsplit;
     const int t0 = split * per, t1 = min(vis.n, t0 + per);
-    for (int t = t0 + warp * KPW * U; t < t1; t += kWarps * KPW * U) {
+    for (int t = t0 + warp * KPW * U; t < t1; t += NW * KPW * U) {
         float4 kf[U], vf[U];
         bool on[U];
 #pragma unroll
@@ -211,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const SwaDecodeArgs
             if (lane == 0) part.m[warp][g] = m[g], part.l[warp][g] = l[g];
         }
     }
-    join<E, D, GC>(part, joined, out, split, nsplit, ng);
+    join<E, D, NW, GC>(part, joined, out, split, nsplit, ng);
 }
 
 // One step of 16 heads x 8 keys (or 8 channels): D += A B, bf16 operands.
@@ -244,20 +267,24 @@ __device__ __forceinline__ uint4 load_stream(const __nv_bfloat16 *p)
 
 // HR x 8 query heads of a CTA: both halves of the matrix instruction's rows, or one (whose
 // registers then let a third CTA onto the SM, and more loads into flight).
-template <int D, int HR>
-__global__ void __launch_bounds__(kWarps * 32, HR == 1 && D == 64 ? 3 : 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
+template <int D, int HR, int NW>
+__global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 : 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
 {
     using E = __nv_bfloat16;
     constexpr int kHeads = 8 * HR;
     constexpr int NC = D / 32;  // 16-byte chunks of a row per lane
-    __shared__ Partials<kHeads, D> part;
-    __shared__ Joined<kHeads, D> joined;
+    using Shared = DecodeShared<NW, kHeads, D>;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    auto &part = reinterpret_cast<Shared *>(dyn)->part;
+    auto &joined = reinterpret_cast<Shared *>(dyn)->joined;
     const int split = blockIdx.x, hk = blockIdx.y / nchunk, chunk = blockIdx.y % nchunk, b = blockIdx.z;
     const int G = a.Hq / a.Hk, g0 = chunk * kHeads, ng = min(kHeads, G - g0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
     E *out = static_cast<E *>(a.o) + ((long long)b * a.Hq + hk * G + g0) * D;
+    cluster_arrive();
     const int P = a.pos[b];
     if (P < 0) {  // no sequence in this row
+        cluster_wait();
         if (split == 0)
             for (int i = threadIdx.x; i < ng * D; i += blockDim.x) out[i] = from_f32<E>(0.f);
         return;
@@ -313,7 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, HR == 1 && D == 64 ? 3 : 2) decod
         load_keys(t);
         load_values(t);
     }
-    for (; t < t1; t += kWarps * 16) {
+    for (; t < t1; t += NW * 16) {
         float s[2][2 * HR] = {};
 #pragma unroll
         for (int j = 0; j < NC; ++j)
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(kWarps * 32, HR == 1 && D == 64 ? 3 : 2) decod
                     mma_bf16(s[r], q[0][j].z, q[0][j].w, kf[r][j].z, kf[r][j].w);
                 }
             }
-        const int tn = t + kWarps * 16;
+        const int tn = t + NW * 16;
         if (tn < t1) load_keys(tn);
         // s[r][0..1]: head gr, keys 8 r + 2 c + {0, 1}; s[r][2..3]: head gr + 8
         float mx[HR];
@@ -410,23 +437,39 @@ __global__ void __launch_bounds__(kWarps * 32, HR == 1 && D == 64 ? 3 : 2) decod
                         make_float4(o[j * 8 + n][2 * h + e], o[j * 8 + n + 1][2 * h + e], o[j * 8 + n + 2][2 * h + e],
                                     o[j * 8 + n + 3][2 * h + e]);
     }
-    join<E, D, kHeads>(part, joined, out, split, nsplit, ng);
+    join<E, D, NW, kHeads>(part, joined, out, split, nsplit, ng);
 }
 
-// `gc` query heads of a group per CTA.  The visible positions of a row are split over a
-// cluster while there are fewer CTAs than four times what runs at once (a grid of that size
-// leaves at most a fifth of a wave behind) and every warp has two steps or more.
-template <typename Kernel>
-cudaError_t launch(Kernel kern, const SwaDecodeArgs &a, int gc, int num_sms, cudaStream_t stream)
+// CTAs that share a (sequence, heads) row: the number with the least waves x time of a
+// CTA, whose own cost (query, join, cluster) counts as much as about 300 positions
+// (64 x 4 rows of 2052 positions of 128 bf16: 103 us split in 8, 78 in 4, 68 in 2).
+int splits(const SwaDecodeArgs &a, int gc, int per_sm, int num_sms)
 {
     const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc;
+    const long long rows = (long long)a.B * a.Hk * nchunk, seen = (long long)a.window + a.sinks, fit = (long long)per_sm * num_sms;
+    int best = 1;
+    double least = 0;
+    for (int n = 1; n <= kMaxSplit; n *= 2) {
+        const double cost = (double)((rows * n + fit - 1) / fit) * ((double)seen / n + 300.0);
+        if (n == 1 || cost < least) least = cost, best = n;
+    }
+    return best;
+}
+
+// GC query heads of a group and NW warps per CTA, PER_SM CTAs on an SM.
+template <auto kern, int GC, int D, int NW, int PER_SM>
+cudaError_t launch(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
+{
+    constexpr int gc = GC, bytes = sizeof(DecodeShared<NW, GC, D>);
+    static std::atomic<unsigned long long> set{0};
+    cudaError_t e = ensure_smem_limit(kern, bytes, set);
+    if (e != cudaSuccess) return e;
+    const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc, nsplit = splits(a, gc, PER_SM, num_sms);
     if ((long long)a.Hk * nchunk > 65535) return cudaErrorInvalidValue;
-    const long long ctas = (long long)a.B * a.Hk * nchunk;
-    int nsplit = 1;
-    while (nsplit < 8 && ctas * nsplit < kFill * num_sms && (a.window + a.sinks) / (nsplit * 2) >= 2 * 16 * kWarps) nsplit *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -441,9 +484,9 @@ template <int D>
 cudaError_t by_group_f32(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
 {
     const int G = a.Hq / a.Hk;
-    if (G == 1) return launch(decode_kernel<float, D, 1>, a, 1, num_sms, stream);
-    if (G == 2) return launch(decode_kernel<float, D, 2>, a, 2, num_sms, stream);
-    return launch(decode_kernel<float, D, 4>, a, 4, num_sms, stream);
+    if (G == 1) return launch<decode_kernel<float, D, 1>, 1, D, 4, 4>(a, num_sms, stream);
+    if (G == 2) return launch<decode_kernel<float, D, 2>, 2, D, 4, 4>(a, num_sms, stream);
+    return launch<decode_kernel<float, D, 4>, 4, D, 4, 4>(a, num_sms, stream);
 }
 
 }  // namespace
@@ -451,9 +494,15 @@ cudaError_t by_group_f32(const SwaDecodeArgs &a, int num_sms, cudaStream_t strea
 cudaError_t launch_swa_decode(const SwaDecodeArgs &a, bool bf16, int num_sms, cudaStream_t stream)
 {
     if (bf16) {
-        if (a.d == 64 && a.Hq / a.Hk <= 8) return launch(decode_mma_kernel<64, 1>, a, 8, num_sms, stream);
-        return a.d == 128 ? launch(decode_mma_kernel<128, 2>, a, 16, num_sms, stream)
-                          : launch(decode_mma_kernel<64, 2>, a, 16, num_sms, stream);
+        // few rows: eight warps a CTA, so that a warp's walk is short (one sequence, 16 heads of
+        // 128, 2052 slots: 13.8 us with four)
+        const bool small_group = a.Hq / a.Hk <= 8;
+        if (small_group && (long long)a.B * a.Hk * kMaxSplit <= num_sms)
+            return a.d == 128 ? launch<decode_mma_kernel<128, 1, 8>, 8, 128, 8, 1>(a, num_sms, stream)
+                              : launch<decode_mma_kernel<64, 1, 8>, 8, 64, 8, 1>(a, num_sms, stream);
+        if (small_group && a.d == 64) return launch<decode_mma_kernel<64, 1, 4>, 8, 64, 4, 4>(a, num_sms, stream);
+        return a.d == 128 ? launch<decode_mma_kernel<128, 2, 4>, 16, 128, 4, 2>(a, num_sms, stream)
+                          : launch<decode_mma_kernel<64, 2, 4>, 16, 64, 4, 2>(a, num_sms, stream);
     }
     return a.d == 128 ? by_group_f32<128>(a, num_sms, stream) : by_group_f32<64>(a, num_sms, stream);
 }
