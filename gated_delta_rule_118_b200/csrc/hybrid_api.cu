@@ -57,7 +57,7 @@ gdn2_status take_strides(const long long *given, const int *sizes, int n, int d,
 gdn2_status check_swa_sizes(int B, int Hq, int Hk, int d, int window, int sinks, float scale)
 {
     if (B <= 0 || Hq <= 0 || Hk <= 0 || d <= 0 || window < 1 || sinks < 0) return GDN2_ERR_SHAPE;
-    if (Hq % Hk != 0 || !(scale > 0.f) || !isfinite(scale)) return GDN2_ERR_SHAPE;
+    if (Hq % Hk != 0 || !(scale >= 1e-30f && scale <= 1e30f)) return GDN2_ERR_SHAPE;  // (lse / scale is formed)
     if (d != 64 && d != 128) return GDN2_ERR_UNSUPPORTED;
     if (B > 65535 || Hq > 65535) return GDN2_ERR_UNSUPPORTED;  // grid y/z limits
     return GDN2_OK;
@@ -71,6 +71,7 @@ gdn2_status swa_args(SwaArgs &a, const void *q, const void *k, const void *v, co
     gdn2_status st = check_swa_sizes(B, Hq, Hk, d, window, sinks, scale);
     if (st != GDN2_OK) return st;
     if (T < 0 || Tk < T) return GDN2_ERR_SHAPE;
+    if (Tk > GDN2_SWA_MAX_TOKENS) return GDN2_ERR_UNSUPPORTED;  // grid z limit
     const int esize = dtype == GDN2_BF16 ? 2 : 4;
     const int nq[3] = {B, T, Hq}, nk[3] = {B, Tk, Hk};
     if ((st = take_strides(strides, nq, 3, d, esize, a.qs)) != GDN2_OK) return st;

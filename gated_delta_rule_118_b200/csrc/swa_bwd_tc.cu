@@ -107,7 +107,8 @@ __device__ __forceinline__ bool put_row(uint32_t tm, float f, E *dst, bool insid
 }
 
 // ---------------------------------------------------------------- dk, dv
-// The work of one CTA along grid x: a key tile and its range of query tiles.
+// The work of one CTA along grid z (slowest, so that the long ranges of all heads start
+// first): a key tile and its range of query tiles.
 struct KvPlan {
     int nseg;      // segments of a sink tile's queries; 0: no splitting
     int seg;       // query tiles of a segment
@@ -135,16 +136,20 @@ struct KvRange {
     }
 };
 
-enum { KV_FULL, QG_FULL, QG_EMPTY = QG_FULL + 2, LD_FULL = QG_EMPTY + 2, LD_EMPTY = LD_FULL + 2,
-       S_FULL = LD_EMPTY + 2, DP_FULL, P_FULL, DS_FULL, DONE, NBAR };
+enum { KV_FULL, QG_FULL, QG_EMPTY = QG_FULL + 2, EXT_FULL = QG_EMPTY + 2, S_FULL = EXT_FULL + 2, DP_FULL, P_FULL, DS_FULL,
+       DONE, NBAR };
 
 template <int D>
 struct KvLayout {
     static constexpr int TILE = Tiles<D>::TILE;
     static constexpr int K = 0, V = TILE, Q = 2 * TILE, G = 4 * TILE;
-    static constexpr int LD = 6 * TILE;            // [stage][lse, delta][128] fp32
-    static constexpr int BAR = LD + 2048;
+    // the sixteen more steps of the inner products that subtract lse and delta: 16-byte rows
+    // of eight steps, [stage][lse, delta][128 rows]; the key tile's; eight steps of zeros
+    static constexpr int EXT = 6 * TILE, MINUS = EXT + 4 * 2048, ZERO = MINUS + 2048;
+    static constexpr int BADS = ZERO + 2048;      // [half][128]
+    static constexpr int BAR = BADS + 1024;
     static constexpr int SLOT = BAR + 8 * NBAR + 8;
+    __host__ __device__ static constexpr int ext(int stage, int which) { return EXT + (stage * 2 + which) * 2048; }
     static constexpr int BYTES = SLOT + 16 + 1024;
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
 };
@@ -159,16 +164,21 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = blockIdx.y, b = blockIdx.z;
+    const int hk = blockIdx.x, b = blockIdx.y;
     const int n = seq_len(a, b), off = a.Tk - a.T, G = a.Hq / a.Hk;
-    const KvRange rg(a, plan, blockIdx.x, n);
+    const KvRange rg(a, plan, blockIdx.z, n);
     const int nq = max(rg.q1 - rg.q0, 0), N = G * nq;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
-    float *ld = reinterpret_cast<float *>(sm + L::LD);
     if (tid == 0) {
-        for (int i = 0; i < NBAR; ++i) mbar_init(bar + i, i == P_FULL || i == DS_FULL || i == LD_EMPTY || i == LD_EMPTY + 1 ? 8 : 1);
+        for (int i = 0; i < NBAR; ++i) mbar_init(bar + i, i == P_FULL || i == DS_FULL ? 8 : 1);
         fence_mbar_init();
+    }
+    if (tid < 128) {  // the key tile's further steps: -1 against the three parts of lse or delta
+        const uint32_t m1 = 0xbf80bf80u;
+        *reinterpret_cast<uint4 *>(sm + L::ZERO + tid * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(sm + L::MINUS + tid * 16) = make_uint4(m1, m1 & 0xffffu, 0, 0);
+        fence_proxy_async_smem();
     }
     if (warp == kMma) {
         tmem_alloc(slot, 512);
@@ -179,8 +189,12 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
     tc_fence_after();
     const uint32_t tmem = *slot;
     const uint32_t sbase = smem_u32(sm);
-    auto head = [&](int i) { return hk * G + i / nq; };
-    auto row0 = [&](int i) { return (rg.q0 + i % nq) * 128; };
+    // the walk over (head, query tile)
+    struct Walk {
+        int h, q, q0, q1;
+        __device__ __forceinline__ void next() { if (++q == q1) q = q0, ++h; }
+    };
+    const Walk start{hk * G, rg.q0, rg.q0, rg.q1};
 
     if (warp >= 8) {
         setmaxnreg_dec<kRegsIssue>();
@@ -192,13 +206,14 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
             }
             __syncwarp();
             int i = 0;
-            for (; i < N; ++i) {
+            Walk w = start;
+            for (; i < N; ++i, w.next()) {
                 const int s = i & 1;
                 if (!__all_sync(~0u, mbar_wait(bar + QG_EMPTY + s, ((i >> 1) & 1) ^ 1, a.err))) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(bar + QG_FULL + s, 2 * L::TILE);
-                    load_tile<D>(sm + L::Q + s * L::TILE, &mq, bar + QG_FULL + s, head(i), row0(i), b);
-                    load_tile<D>(sm + L::G + s * L::TILE, &mg, bar + QG_FULL + s, head(i), row0(i), b);
+                    load_tile<D>(sm + L::Q + s * L::TILE, &mq, bar + QG_FULL + s, w.h, w.q * 128, b);
+                    load_tile<D>(sm + L::G + s * L::TILE, &mg, bar + QG_FULL + s, w.h, w.q * 128, b);
                 }
                 __syncwarp();
             }
@@ -206,53 +221,78 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
             mbar_wait(bar + KV_FULL, 0, a.err);
             for (int c = max(i - 2, 0); c < i; ++c) mbar_wait(bar + QG_FULL + (c & 1), (c >> 1) & 1, a.err);
         } else if (warp == kRows) {
-            // lse (in log2, +infinity for rows without a token or without a finite score, so
-            // that their probabilities come out 0) and delta of the tile's rows
-            for (int i = 0; i < N; ++i) {
+            // lse / scale and delta of the tile's rows, each as three bf16 parts (their sum is
+            // within 2^-24 of it), subtracted by the products themselves.  Rows without a token
+            // or without a finite score get 2^100, so that their probabilities come out 0.
+            auto split = [](float x) {
+                const float hi = __bfloat162float(__float2bfloat16_rn(x)), mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+                const __nv_bfloat162 u = __floats2bfloat162_rn(hi, mid);
+                const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn((x - hi) - mid));
+                return make_uint4(*reinterpret_cast<const uint32_t *>(&u), lo, 0, 0);
+            };
+            const float inv = 1.f / a.scale;
+            Walk w = start;
+            for (int i = 0; i < N; ++i, w.next()) {
                 const int s = i & 1;
-                if (!__all_sync(~0u, mbar_wait(bar + LD_EMPTY + s, ((i >> 1) & 1) ^ 1, a.err))) break;
-                const long long at = ((long long)b * a.Hq + head(i)) * a.T;
+                const long long at = ((long long)b * a.Hq + w.h) * a.T;
+                float l[4], d[4];
 #pragma unroll
-                for (int x = lane; x < 128; x += 32) {
-                    const int row = row0(i) + x;
-                    const float l = row < n ? a.lse[at + row] : -INFINITY;
-                    ld[s * 256 + x] = l == -INFINITY ? INFINITY : l * kLog2E;
-                    ld[s * 256 + 128 + x] = row < n ? a.delta[at + row] : 0.f;
+                for (int x = 0; x < 4; ++x) {
+                    const int row = w.q * 128 + x * 32 + lane;
+                    l[x] = row < n ? a.lse[at + row] : -INFINITY;
+                    d[x] = row < n ? a.delta[at + row] : 0.f;
                 }
+                if (!__all_sync(~0u, mbar_wait(bar + QG_EMPTY + s, ((i >> 1) & 1) ^ 1, a.err))) break;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    *reinterpret_cast<uint4 *>(sm + L::ext(s, 0) + (x * 32 + lane) * 16) =
+                        l[x] == -INFINITY ? make_uint4(0x7180u, 0, 0, 0) : split(l[x] * inv);
+                    *reinterpret_cast<uint4 *>(sm + L::ext(s, 1) + (x * 32 + lane) * 16) = split(d[x]);
+                }
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar + LD_FULL + s);
+                if (lane == 0) mbar_arrive(bar + EXT_FULL + s);
             }
         } else if (warp == kMma && N > 0) {
             const uint64_t dk = smem_desc(sbase + L::K, 16, 1024, kSw128), dv = smem_desc(sbase + L::V, 16, 1024, kSw128);
             const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dg = smem_desc(sbase + L::G, 16, 1024, kSw128);
             const uint64_t qt = smem_desc(sbase + L::Q, 16384, 1024, kSw128), gt = smem_desc(sbase + L::G, 16384, 1024, kSw128);
             constexpr uint32_t STEP = Tiles<D>::STEP;
-            bool ok = mbar_wait(bar + KV_FULL, 0, a.err) && mbar_wait(bar + QG_FULL, 0, a.err);
+            const uint64_t minus = smem_desc(sbase + L::MINUS, (uint32_t)(L::ZERO - L::MINUS), 128, kSwNone);
+            // S^T less lse / scale, and dP^T less delta, of stage s
+            auto scores = [&](uint32_t s) {
+                issue_rows<D>(tmem + L::TM_S, dk, dq + s * STEP);
+                umma_bf16(tmem + L::TM_S, minus, smem_desc(sbase + L::ext(s, 0), L::ZERO - L::ext(s, 0), 128, kSwNone),
+                          idesc_bf16(128, 128, 0, 0), 1);
+                umma_commit(bar + S_FULL);
+            };
+            auto dots = [&](uint32_t s) {
+                issue_rows<D>(tmem + L::TM_DP, dv, dg + s * STEP);
+                umma_bf16(tmem + L::TM_DP, minus, smem_desc(sbase + L::ext(s, 1), L::ZERO - L::ext(s, 1), 128, kSwNone),
+                          idesc_bf16(128, 128, 0, 0), 1);
+                umma_commit(bar + DP_FULL);
+            };
+            bool ok = mbar_wait(bar + KV_FULL, 0, a.err) && mbar_wait(bar + QG_FULL, 0, a.err) && mbar_wait(bar + EXT_FULL, 0, a.err);
             ok = __all_sync(~0u, ok);
             if (ok) {
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_rows<D>(tmem + L::TM_S, dk, dq);
-                    umma_commit(bar + S_FULL);
-                    issue_rows<D>(tmem + L::TM_DP, dv, dg);
-                    umma_commit(bar + DP_FULL);
+                    scores(0);
+                    dots(0);
                 }
                 __syncwarp();
             }
             for (int i = 0; ok && i < N; ++i) {
                 const uint32_t s = i & 1, sn = s ^ 1;
                 const bool next = i + 1 < N;
-                ok = mbar_wait(bar + P_FULL, s, a.err);
-                if (ok && next) ok = mbar_wait(bar + QG_FULL + sn, ((i + 1) >> 1) & 1, a.err);
-                ok = __all_sync(~0u, ok);
+                if (next)
+                    ok = mbar_wait(bar + QG_FULL + sn, ((i + 1) >> 1) & 1, a.err) && mbar_wait(bar + EXT_FULL + sn, ((i + 1) >> 1) & 1, a.err);
+                ok = __all_sync(~0u, ok && mbar_wait(bar + P_FULL, s, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
                     issue_cols<D>(tmem + L::TM_DV, tmem + L::TM_S, gt + s * STEP, i > 0);
-                    if (next) {  // over P^T, which the product just issued reads: products run in order
-                        issue_rows<D>(tmem + L::TM_S, dk, dq + sn * STEP);
-                        umma_commit(bar + S_FULL);
-                    }
+                    if (next) scores(sn);  // over P^T, which the product just issued reads: products run in order
                 }
                 __syncwarp();
                 ok = __all_sync(~0u, mbar_wait(bar + DS_FULL, s, a.err));
@@ -261,10 +301,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 if (elect_one()) {
                     issue_cols<D>(tmem + L::TM_DK, tmem + L::TM_DP, qt + s * STEP, i > 0);
                     umma_commit(bar + QG_EMPTY + s);
-                    if (next) {
-                        issue_rows<D>(tmem + L::TM_DP, dv, dg + sn * STEP);
-                        umma_commit(bar + DP_FULL);
-                    }
+                    if (next) dots(sn);
                 }
                 __syncwarp();
             }
@@ -279,35 +316,31 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
         const uint32_t ts = lane_base + L::TM_S + hf * 64, tp = lane_base + L::TM_DP + hf * 64;
         const float sc = a.scale * kLog2E;
         bool ok = true;
-        for (int i = 0; i < N; ++i) {
-            const int s = i & 1, i0 = row0(i), c0 = i0 + hf * 64;
-            const float *lse2 = ld + s * 256 + hf * 64, *delta = lse2 + 128;
-            ok = mbar_wait(bar + LD_FULL + s, (i >> 1) & 1, a.err) && mbar_wait(bar + S_FULL, s, a.err);
-            ok = __all_sync(~0u, ok);
+        // query tiles whose rows all hold a token and see all of these keys: first rows [lo, hi]
+        const int full_lo = rg.j0 + 127 - off;
+        const int full_hi = rg.j0 + 128 <= a.sinks ? n - 128 : min(n - 128, a.window - 128 + rg.j0 - off);
+        Walk w = start;
+        for (int i = 0; i < N; ++i, w.next()) {
+            const int s = i & 1, i0 = w.q * 128;
+            ok = __all_sync(~0u, mbar_wait(bar + S_FULL, s, a.err));
             if (!ok) break;
             tc_fence_after();
             float p[64];
             tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(p));
             tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(p + 32));
             tmem_ld_wait(p);
-            // (rows behind the length have p = 0 by their lse, but what stands in their dO
-            // must not reach the product with it)
-            const bool full = i0 + 128 <= n && tile_full(off + i0, off + i0 + 127, rg.j0, rg.j0 + 128, a.window, a.sinks);
-            if (!full) {
-                const int lo = j - off - c0;
+            const bool full = i0 >= full_lo && i0 <= full_hi;
+            if (__builtin_expect(!full, 0)) {
+                // (rows behind the length have p = 0 by their lse, but what stands in their q
+                // and dO must not reach the exponential or the product with it)
+                const int c0 = i0 + hf * 64, lo = j - off - c0;
                 const long long far = (long long)lo + a.window;
                 const int hi = j < a.sinks || far > n - c0 ? n - c0 : (int)far;
 #pragma unroll
                 for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : -INFINITY;
             }
 #pragma unroll
-            for (int x = 0; x < 64; x += 4) {
-                const float4 e = *reinterpret_cast<const float4 *>(lse2 + x);
-                p[x] = ex2_approx(fmaf(p[x], sc, -e.x));
-                p[x + 1] = ex2_approx(fmaf(p[x + 1], sc, -e.y));
-                p[x + 2] = ex2_approx(fmaf(p[x + 2], sc, -e.z));
-                p[x + 3] = ex2_approx(fmaf(p[x + 3], sc, -e.w));
-            }
+            for (int x = 0; x < 64; ++x) p[x] = ex2_approx(p[x] * sc);
             put_bf16(ts, p);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + P_FULL);
@@ -318,23 +351,15 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
             tmem_ld32(tp, *reinterpret_cast<float(*)[32]>(g));
             tmem_ld32(tp + 32, *reinterpret_cast<float(*)[32]>(g + 32));
             tmem_ld_wait(g);
-#pragma unroll
-            for (int x = 0; x < 64; x += 4) {
-                const float4 e = *reinterpret_cast<const float4 *>(delta + x);
-                g[x] = p[x] * (g[x] - e.x);
-                g[x + 1] = p[x + 1] * (g[x + 1] - e.y);
-                g[x + 2] = p[x + 2] * (g[x + 2] - e.z);
-                g[x + 3] = p[x + 3] * (g[x + 3] - e.w);
-            }
-            if (!full)
+            if (__builtin_expect(!full, 0)) {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) g[x] = p[x] == 0.f ? 0.f : g[x];
+            }
+#pragma unroll
+            for (int x = 0; x < 64; ++x) g[x] *= p[x];
             put_bf16(tp, g);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar + DS_FULL);
-                mbar_arrive(bar + LD_EMPTY + s);
-            }
+            if (lane == 0) mbar_arrive(bar + DS_FULL);
         }
         if (ok && N > 0) ok = mbar_wait(bar + DONE, 0, a.err);
         ok = named_bar_and(1, 256, ok);
@@ -350,7 +375,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 const long long at = (((long long)b * a.Tk + j) * a.Hk + hk) * D + hf * (D / 2);
                 bool bad = put_row<D>(tk, a.scale, static_cast<bf16 *>(a.dk) + at, inside, true, have);
                 bad |= put_row<D>(tv, 1.f, static_cast<bf16 *>(a.dv) + at, inside, true, have);
-                uint32_t *bads = reinterpret_cast<uint32_t *>(ld);  // (no more rows of lse are read)
+                uint32_t *bads = reinterpret_cast<uint32_t *>(sm + L::BADS);
                 bads[hf * 128 + r] = bad;
                 named_bar(1, 256);
                 unsigned todo = __ballot_sync(~0u, hf == 0 && (bads[r] | bads[128 + r]));
@@ -395,13 +420,14 @@ __global__ void __launch_bounds__(256) sink_sum_kernel(const __grid_constant__ S
 }
 
 // ---------------------------------------------------------------- dq
-enum { QD_FULL, K_FULL, K_EMPTY = K_FULL + 2, V_FULL = K_EMPTY + 2, V_EMPTY = V_FULL + 2, SQ_FULL = V_EMPTY + 2, SQ_FREE,
+enum { QD_FULL, K_FULL, K_EMPTY = K_FULL + 3, V_FULL = K_EMPTY + 3, V_EMPTY, SQ_FULL, SQ_FREE,
        DPQ_FULL, DSQ_FULL = DPQ_FULL + 2, DONE_Q = DSQ_FULL + 2, NBAR_Q };
 
 template <int D>
 struct QLayout {
     static constexpr int TILE = Tiles<D>::TILE;
-    static constexpr int Q = 0, G = TILE, K = 2 * TILE, V = 4 * TILE;
+    // three stages of K, which dQ reads last, and one of V, which only dP reads
+    static constexpr int Q = 0, G = TILE, K = 2 * TILE, V = 5 * TILE;
     static constexpr int BAD = 6 * TILE;           // [half][128]
     static constexpr int BAR = BAD + 1024;
     static constexpr int SLOT = BAR + 8 * NBAR_Q + 8;
@@ -419,7 +445,7 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int i0 = (gridDim.x - 1 - blockIdx.x) * 128, h = blockIdx.y, b = blockIdx.z;  // longest rows first
+    const int i0 = (gridDim.z - 1 - blockIdx.z) * 128, h = blockIdx.x, b = blockIdx.y;  // longest rows first
     const int n = seq_len(a, b), off = a.Tk - a.T, hk = h / (a.Hq / a.Hk);
     if (i0 >= n) {  // padding only
         const int rows = min(128, a.T - i0);
@@ -455,29 +481,29 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
                 load_tile<D>(sm + L::G, &mg, bar + QD_FULL, h, i0, b);
             }
             __syncwarp();
-            int nk = 0, nv = 0;
+            int nk = 0, nv = 0, ks = 0;
+            uint32_t kph = 1;
             for (int c = 0; c < N; ++c) {
-                const int s = c & 1;
-                const uint32_t ph = ((c >> 1) & 1) ^ 1;
-                if (!__all_sync(~0u, mbar_wait(bar + K_EMPTY + s, ph, a.err))) break;
+                if (!__all_sync(~0u, mbar_wait(bar + K_EMPTY + ks, kph, a.err))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(bar + K_FULL + s, L::TILE);
-                    load_tile<D>(sm + L::K + s * L::TILE, &mk, bar + K_FULL + s, hk, kt.tile(c) * 128, b);
+                    mbar_arrive_expect_tx(bar + K_FULL + ks, L::TILE);
+                    load_tile<D>(sm + L::K + ks * L::TILE, &mk, bar + K_FULL + ks, hk, kt.tile(c) * 128, b);
                 }
                 __syncwarp();
                 nk = c + 1;
-                if (!__all_sync(~0u, mbar_wait(bar + V_EMPTY + s, ph, a.err))) break;
+                if (!__all_sync(~0u, mbar_wait(bar + V_EMPTY, (c & 1) ^ 1, a.err))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(bar + V_FULL + s, L::TILE);
-                    load_tile<D>(sm + L::V + s * L::TILE, &mv, bar + V_FULL + s, hk, kt.tile(c) * 128, b);
+                    mbar_arrive_expect_tx(bar + V_FULL, L::TILE);
+                    load_tile<D>(sm + L::V, &mv, bar + V_FULL, hk, kt.tile(c) * 128, b);
                 }
                 __syncwarp();
                 nv = c + 1;
+                if (++ks == 3) ks = 0, kph ^= 1;
             }
             // every copy has landed before the CTA ends, also when another role gave up
             mbar_wait(bar + QD_FULL, 0, a.err);
-            for (int c = max(nk - 2, 0); c < nk; ++c) mbar_wait(bar + K_FULL + (c & 1), (c >> 1) & 1, a.err);
-            for (int c = max(nv - 2, 0); c < nv; ++c) mbar_wait(bar + V_FULL + (c & 1), (c >> 1) & 1, a.err);
+            for (int c = max(nk - 3, 0); c < nk; ++c) mbar_wait(bar + K_FULL + c % 3, (c / 3) & 1, a.err);
+            if (nv > 0) mbar_wait(bar + V_FULL, (nv - 1) & 1, a.err);
         } else if (warp == kMma) {
             const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dg = smem_desc(sbase + L::G, 16, 1024, kSw128);
             const uint64_t dk = smem_desc(sbase + L::K, 16, 1024, kSw128), dv = smem_desc(sbase + L::V, 16, 1024, kSw128);
@@ -486,23 +512,32 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
             bool ok = mbar_wait(bar + QD_FULL, 0, a.err);
             // S and dP of tile c; S goes over the S that has been read, dP into the buffer whose
             // dS was the operand of a product issued before
+            uint32_t ks = 0, kph = 0;  // K stage of the next scores
             auto scores = [&](int c) {
-                const uint32_t s = c & 1, ph = (c >> 1) & 1;
-                ok = ok && mbar_wait(bar + K_FULL + s, ph, a.err) && mbar_wait(bar + V_FULL + s, ph, a.err);
+                const uint32_t s = c & 1;
+                ok = ok && mbar_wait(bar + K_FULL + ks, kph, a.err);
                 if (c > 0) ok = ok && mbar_wait(bar + SQ_FREE, (c - 1) & 1, a.err);
                 ok = __all_sync(~0u, ok);
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_rows<D>(tmem + L::TM_S, dq, dk + s * STEP);
+                    issue_rows<D>(tmem + L::TM_S, dq, dk + ks * STEP);
                     umma_commit(bar + SQ_FULL);
-                    issue_rows<D>(tmem + L::TM_DP + s * 128, dg, dv + s * STEP);
-                    umma_commit(bar + DPQ_FULL + s);
-                    umma_commit(bar + V_EMPTY + s);
                 }
                 __syncwarp();
+                ok = __all_sync(~0u, mbar_wait(bar + V_FULL, s, a.err));
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_rows<D>(tmem + L::TM_DP + s * 128, dg, dv);
+                    umma_commit(bar + DPQ_FULL + s);
+                    umma_commit(bar + V_EMPTY);
+                }
+                __syncwarp();
+                if (++ks == 3) ks = 0, kph ^= 1;
             };
             scores(0);
+            uint32_t kd = 0;           // K stage of the next dQ
             for (int c = 0; ok && c < N; ++c) {
                 const uint32_t s = c & 1;
                 if (c + 1 < N) scores(c + 1);
@@ -510,10 +545,11 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_cols<D>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + s * STEP, c > 0);
-                    umma_commit(bar + K_EMPTY + s);
+                    issue_cols<D>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + kd * STEP, c > 0);
+                    umma_commit(bar + K_EMPTY + kd);
                 }
                 __syncwarp();
+                if (++kd == 3) kd = 0;
             }
             if (elect_one()) umma_commit(bar + DONE_Q);
             __syncwarp();
@@ -530,7 +566,7 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
         const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2E;
         bool ok = true;
         for (int c = 0; c < N; ++c) {
-            const int s = c & 1, j0 = kt.tile(c) * 128, c0 = j0 + hf * 64;
+            const int s = c & 1, j0 = kt.tile(c) * 128;
             const uint32_t tp = lane_base + L::TM_DP + s * 128 + hf * 64;
             ok = __all_sync(~0u, mbar_wait(bar + SQ_FULL, s, a.err));
             if (!ok) break;
@@ -543,8 +579,8 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + SQ_FREE);
             const bool full = tile_full(off + i0, off + i0 + 127, j0, j0 + 128, a.window, a.sinks);
-            if (!full) {
-                const int hi = p_ - c0, lo = p_ - a.window + 1 - c0, sk = a.sinks - c0;
+            if (__builtin_expect(!full, 0)) {
+                const int c0 = j0 + hf * 64, hi = p_ - c0, lo = p_ - a.window + 1 - c0, sk = a.sinks - c0;
 #pragma unroll
                 for (int x = 0; x < 64; ++x) p[x] = x <= hi && (x >= lo || x < sk) ? p[x] : -INFINITY;
             }
@@ -559,9 +595,10 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
             tmem_ld_wait(g);
 #pragma unroll
             for (int x = 0; x < 64; ++x) g[x] = p[x] * (g[x] - delta);
-            if (!full)
+            if (__builtin_expect(!full, 0)) {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) g[x] = p[x] == 0.f ? 0.f : g[x];
+            }
             put_bf16(tp, g);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + DSQ_FULL + s);
@@ -622,9 +659,9 @@ cudaError_t impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream
         !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128) || !make_rows_map(&mg, a.dO, D, a.Hq, a.T, a.B, gs, 128))
         return cudaErrorInvalidValue;
     const int items = plan.nseg ? plan.nsink * plan.nseg + plan.ntiles - plan.nsink : plan.ntiles;
-    dkdv_tc_kernel<D><<<dim3(items, a.Hk, a.B), kThreads, KvLayout<D>::BYTES, stream>>>(a, plan, mq, mk, mv, mg);
+    dkdv_tc_kernel<D><<<dim3(a.Hk, a.B, items), kThreads, KvLayout<D>::BYTES, stream>>>(a, plan, mq, mk, mv, mg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    dq_tc_kernel<D><<<dim3((a.T + 127) / 128, a.Hq, a.B), kThreads, QLayout<D>::BYTES, stream>>>(a, mq, mk, mv, mg);
+    dq_tc_kernel<D><<<dim3(a.Hq, a.B, (a.T + 127) / 128), kThreads, QLayout<D>::BYTES, stream>>>(a, mq, mk, mv, mg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (plan.nseg && plan.nsink) {
         sink_sum_kernel<D><<<dim3(plan.nsink * 16, a.Hk, a.B), 256, 0, stream>>>(a, plan);

@@ -11,7 +11,8 @@
 // backward), and 0 * NaN or 0 * infinity is NaN.  Scrubbing every tile would cost
 // shared-memory bandwidth on every call, so a kernel instead looks at the row it
 // is about to write: if it is not finite, the row is computed again from memory by
-// one of the functions below, which touch visible keys only.  Finite inputs never
+// one of the functions below, which touch visible keys only (unless its own row holds a
+// NaN, which reaches all of it).  Finite inputs never
 // take that path; a row that is NaN by its own visible inputs comes out NaN again.
 #pragma once
 
@@ -83,6 +84,20 @@ __device__ __forceinline__ float dot_rows(const E *x, const E *y)
     return s;
 }
 
+// Whether a row holds a NaN (the whole warp asks): what is formed from such a row is NaN
+// throughout, and need not be formed again.
+template <typename E, int D>
+__device__ __forceinline__ bool has_nan(const E *row)
+{
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        const float x = to_f32(row[(threadIdx.x & 31) + 32 * u]);
+        bad |= x != x;
+    }
+    return __any_sync(~0u, bad);
+}
+
 // Element pointers of one (batch, head).
 template <typename E>
 struct Rows {
@@ -107,6 +122,7 @@ __device__ __forceinline__ void row_forward(const SwaArgs &a, int b, int h, int 
 {
     const int lane = threadIdx.x & 31, p = a.Tk - a.T + i;
     const E *q = rows_of<E>(a.q, a.qs, b, h)[i];
+    if (has_nan<E, D>(q)) return;
     const int hk = h / (a.Hq / a.Hk);
     const Rows<E> k = rows_of<E>(a.k, a.ks, b, hk), v = rows_of<E>(a.v, a.vs, b, hk);
     const int lo = p - a.window + 1 > 0 ? p - a.window + 1 : 0;
@@ -151,6 +167,7 @@ __device__ __forceinline__ void row_dq(const SwaArgs &a, int b, int h, int i)
     const int lane = threadIdx.x & 31, p = a.Tk - a.T + i;
     const E *q = rows_of<E>(a.q, a.qs, b, h)[i];
     const E *g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D)[i];
+    if (has_nan<E, D>(q) || has_nan<E, D>(g)) return;
     const int hk = h / (a.Hq / a.Hk);
     const Rows<E> k = rows_of<E>(a.k, a.ks, b, hk), v = rows_of<E>(a.v, a.vs, b, hk);
     const long long row = ((long long)b * a.Hq + h) * a.T + i;
@@ -186,6 +203,7 @@ __device__ __forceinline__ void row_dkdv(const SwaArgs &a, int b, int hk, int j)
     const int i0 = j > off ? j - off : 0;
     const long long far = (long long)j + a.window - off;  // first row that no longer sees j through the window
     const int i1 = (j < a.sinks || far > len) ? len : (int)far;
+    if (i0 < i1 && has_nan<E, D>(k)) return;
     float dk[D / 32] = {}, dv[D / 32] = {};
     for (int h = hk * G; h < hk * G + G; ++h) {
         const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D);

@@ -60,11 +60,12 @@ enum { Q_FULL, Q_EMPTY, K_FULL, K_EMPTY = K_FULL + 2, V_FULL = K_EMPTY + 2, V_EM
        N_FULL = O_LAST + 2, N_EMPTY, DRAINED, NBAR };
 constexpr int kReaders = 11;      // warps that read the launch control's answer
 
-// The 256 query rows of one block of the grid, longest rows first.
+// The 256 query rows of one block of the grid: the rows that see most keys first, of all
+// heads and sequences, so that the short ones fill the gaps at the end.
 struct Work {
     int i0, h, b, n;
     __device__ __forceinline__ Work(const SwaArgs &a, int x, int y, int z)
-        : i0((gridDim.x - 1 - x) * 256), h(y), b(z), n(seq_len(a, z)) {}
+        : i0((gridDim.z - 1 - z) * 256), h(x), b(y), n(seq_len(a, y)) {}
     __device__ __forceinline__ KeyTiles tiles(const SwaArgs &a) const
     {
         const int off = a.Tk - a.T;
@@ -409,7 +410,7 @@ cudaError_t impl(const SwaArgs &a, cudaStream_t stream)
     if (!make_rows_map(&mq, a.q, D, a.Hq, a.T, a.B, a.qs, 128) || !make_rows_map(&mk, a.k, D, a.Hk, a.Tk, a.B, a.ks, 128) ||
         !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128))
         return cudaErrorInvalidValue;
-    kern<<<dim3((a.T + 255) / 256, a.Hq, a.B), kThreads, L::BYTES, stream>>>(a, mq, mk, mv);
+    kern<<<dim3(a.Hq, a.B, (a.T + 255) / 256), kThreads, L::BYTES, stream>>>(a, mq, mk, mv);
     return cudaGetLastError();
 }
 

@@ -338,8 +338,8 @@ gdn2_status gdn2_bwd_chunked(const void *q, const void *k, const void *v,
  *               k, then of v; NULL means dense.  The d elements of a row are always
  *               contiguous; a stride is a multiple of 16 bytes and at least d.
  *               Strides of an axis of size 1 are ignored.
- *   d 64 or 128; Hq a multiple of Hk; 0 <= T <= Tk; window >= 1; 0 <= sinks;
- *   scale > 0 and finite.
+ *   d 64 or 128; Hq a multiple of Hk; 0 <= T <= Tk <= GDN2_SWA_MAX_TOKENS;
+ *   window >= 1; 0 <= sinks; 1e-30 <= scale <= 1e30.
  *
  * A row whose visible scores are all -infinity gives o = 0 and lse = -infinity.
  * What stands in places that a row does not see (keys behind the window or ahead
@@ -348,6 +348,7 @@ gdn2_status gdn2_bwd_chunked(const void *q, const void *k, const void *v,
  * probabilities rounded to bf16 for the product with v); fp32 inputs in fp32 on
  * the CUDA cores.
  */
+#define GDN2_SWA_MAX_TOKENS 4194304
 gdn2_status gdn2_swa_fwd(const void *q, const void *k, const void *v, const int *lens, void *o, float *lse,
                          int B, int T, int Tk, int Hq, int Hk, int d, int window, int sinks, float scale,
                          const long long *strides, gdn2_dtype dtype, gdn2_stream_t stream);
