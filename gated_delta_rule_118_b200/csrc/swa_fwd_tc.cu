@@ -1,25 +1,30 @@
 // swa_fwd_tc.cu -- windowed attention forward for bf16 on the tensor cores.
 //
 // A CTA takes 256 query rows of a head at a time, as two tiles of 128 rows that share
-// every key and value tile of 128 keys.  One warp loads tiles by TMA (two-stage rings of
-// K and of V), one issues the products, and a warpgroup per query tile does the softmax,
-// one row per thread:
+// every key and value tile of 128 keys, and works in blocks of 64 keys.  One warp loads
+// tiles by TMA (two-stage rings of K and of V); for each query tile a warp issues the
+// products and a warpgroup does the softmax, one row per thread:
 //   S = Q K^T            operands in shared memory, S in tensor memory
 //   P = exp2(S - m)      read from tensor memory, written back over S as bf16
 //   O += P V             A operand straight from tensor memory
-// While one tile is in its softmax the tensor core works on the other tile, so the
-// pair runs at the slower of the two.  Bound by that alternation: a 128 x 128 tile is
-// 16384 exponentials, 1024 cycles of the SM's special function units, as many as its two
-// products take on the tensor core, and each hand-over adds its latency.
+// Each query tile has two score buffers: the scores of block u + 1 are computed while
+// block u is in its softmax.  What bounds the kernel is the chain of hand-overs (a product's
+// completion takes about 335 cycles to be seen, a barrier about 100): with one buffer of
+// 128 keys a tile, kernels with a quarter of the products and no exponentials took 70 % of
+// the time.  Two tiles x two buffers keep four chains in flight.
 //
 // CTAs are persistent: a CTA that finishes asks the hardware for a block that has not
 // started (cluster launch control) and runs it, so the next rows' loads and first scores
 // overlap the last rows' writes.
 //
-// The running maximum is only raised (and O rescaled in tensor memory) when a row
-// outgrows its reference by more than 2^8: with the reference in the exponent of
-// every term and in the final sum alike, any reference gives the same result as
-// long as nothing overflows, and P is rounded relative to its own size.
+// A row's reference m need not be its maximum: it stands in the exponent of every term
+// and in the final sum alike, P is rounded relative to its own size, and fp32 and bf16
+// reach to 2^127.  So a row takes its reference from the first tile it sees and keeps it;
+// later tiles whose keys are all visible are exponentiated without looking for a maximum
+// first (which was a quarter of the softmax), and only a tile whose sum comes out at 2^60
+// or more, or not finite, is taken again with a new reference (and O rescaled in tensor
+// memory).  Tiles with masked keys look for their maximum, and raise the reference when a
+// row outgrows it by more than 2^8.
 // P is rounded to bf16 for the product (at most 2^-8 relative, as the operand of
 // a bf16 tensor core has to be); the row sum adds the unrounded values in fp32.
 #include <cuda.h>
@@ -36,11 +41,12 @@ using namespace swa;
 using namespace sm100;
 
 constexpr int kThreads = 384;  // two softmax warpgroups, then the issuing warps
-constexpr int kTma = 8, kMma = 9, kNext = 10;
-// 384 threads launch with 168 registers each; a softmax row keeps 128 scores in
-// registers, the issuing warps need few: 2 x 128 x 216 + 128 x 72 = 384 x 168.
-constexpr int kRegsSoftmax = 216, kRegsIssue = 72;
-constexpr float kMaxGrowth = 8.f;  // log2
+constexpr int kTma = 8, kNext = 9, kMma = 10;  // kMma + t issues the products of query tile t
+// 384 threads launch with 168 registers each; a softmax row keeps 64 scores and their
+// exponentials in registers, the issuing warps need fewer: 2 x 128 x 200 + 128 x 104 = 384 x 168.
+constexpr int kRegsSoftmax = 200, kRegsIssue = 104;
+constexpr float kMaxGrowth = 8.f;         // log2
+constexpr float kMaxSum = 0x1p60f;        // of a tile exponentiated by an old reference
 
 template <int D>
 struct Layout {
@@ -49,16 +55,22 @@ struct Layout {
     static constexpr int NEXT = BAR + 256;         // answer of the launch control
     static constexpr int SLOT = NEXT + 16;
     static constexpr int BYTES = SLOT + 16 + 1024;
-    static constexpr uint32_t TM_O = 256;          // scores of tile t at 128 t, then the outputs
+    static constexpr uint32_t TM_O = 256;          // scores of tile t at 128 t (two buffers of 64), then the outputs
 };
 
 // mbarriers
 enum { Q_FULL, Q_EMPTY, K_FULL, K_EMPTY = K_FULL + 2, V_FULL = K_EMPTY + 2, V_EMPTY = V_FULL + 2,
-       S_FULL = V_EMPTY + 2,      // [tile]: scores are there, and the product P V before them is in O
-       P_FULL = S_FULL + 2,       // [tile], one arrival of each softmax warp
-       O_LAST = P_FULL + 2,       // [tile]: the last product of these rows is in O
-       N_FULL = O_LAST + 2, N_EMPTY, DRAINED, NBAR };
-constexpr int kReaders = 11;      // warps that read the launch control's answer
+       S_FULL = V_EMPTY + 2,      // [tile][buffer]
+       P_FULL = S_FULL + 4,       // [tile][buffer], one arrival of each softmax warp
+       O_DONE = P_FULL + 4,       // [tile]: a product P V is in O
+       O_LAST = O_DONE + 2,       // [tile]: the last one of these rows is
+       N_FULL = O_LAST + 2, N_EMPTY, DRAINED, NBAR = DRAINED + 2 };
+// released by the issuing warps of both query tiles
+__host__ __device__ constexpr bool both_tiles(int i)
+{
+    return i == Q_EMPTY || i == K_EMPTY || i == K_EMPTY + 1 || i == V_EMPTY || i == V_EMPTY + 1;
+}
+constexpr int kReaders = 12;      // warps that read the launch control's answer
 
 // The 256 query rows of one block of the grid: the rows that see most keys first, of all
 // heads and sequences, so that the short ones fill the gaps at the end.
@@ -73,17 +85,23 @@ struct Work {
     }
 };
 
-// The tiles of 128 keys that one query tile visits.
+// The blocks of 64 keys that one query tile visits, and those all of whose keys all of
+// its rows see.
 struct Visits {
-    int w0, ns, last;
+    int w0, ns, last;        // visited: [w0, last], and below ns
+    int wf, nf, lf;          // full: [wf, lf], and below nf up to lf
     __device__ __forceinline__ Visits(const SwaArgs &a, int i0, int n)
     {
         const int p0 = a.Tk - a.T + i0, p1 = a.Tk - a.T + min(i0 + 128, n) - 1;
-        w0 = (p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0) >> 7;
-        ns = (a.sinks + 127) >> 7;
-        last = i0 < n ? p1 >> 7 : -1;  // -1: no row of this tile holds a token
+        w0 = (p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0) >> 6;
+        ns = (a.sinks + 63) >> 6;
+        last = i0 < n ? p1 >> 6 : -1;  // -1: no row of this tile holds a token
+        wf = p0 + 127 - a.window < 0 ? 0 : ((p0 + 127 - a.window) >> 6) + 1;
+        nf = a.sinks >> 6;
+        lf = (p0 - 63) >> 6;
     }
     __device__ __forceinline__ bool operator()(int j) const { return j <= last && (j >= w0 || j < ns); }
+    __device__ __forceinline__ bool full(int j) const { return j <= lf && (j >= wf || j < nf); }
 };
 
 template <int D>
@@ -101,7 +119,7 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
     static_assert(NBAR * 8 <= 256, "room for the barriers");
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i)
-            mbar_init(bar + i, i == P_FULL || i == P_FULL + 1 ? 4 : i == N_EMPTY ? kReaders : 1);
+            mbar_init(bar + i, i >= P_FULL && i < P_FULL + 4 ? 4 : i == N_EMPTY ? kReaders : both_tiles(i) ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == kMma) {
@@ -189,84 +207,92 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
                 mbar_wait(bar + V_FULL + (c & 1), (c >> 1) & 1, a.err);
             }
             if (qph || kt_count) mbar_wait(bar + Q_FULL, qph ^ 1, a.err);
-        } else if (warp == kMma) {
+        } else if (warp >= kMma) {
             // the whole warp walks the loop and one lane issues: the descriptors stay in
             // uniform registers (computed in one lane's registers every product cost about
             // 100 cycles of issue)
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
-            const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dk = smem_desc(sbase + L::K, 16, 1024, kSw128);
-            const uint64_t dv = smem_desc(sbase + L::V, 16384, 1024, kSw128);
+            const int t = warp - kMma;
+            const uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
             constexpr uint32_t STEP = L::TILE >> 4;  // descriptor units (16 bytes) of a tile
-            uint32_t kc = 0, qph = 0, pph[2] = {0, 0};  // tiles consumed, phases
+            const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128) + t * STEP, dk = smem_desc(sbase + L::K, 16, 1024, kSw128);
+            const uint64_t dv = smem_desc(sbase + L::V, 16384, 1024, kSw128);
+            const uint32_t ts = tmem + t * 128, to = tmem + L::TM_O + t * D;
+            uint32_t kc = 0, vc = 0, qph = 0;        // tiles consumed, blocks of the grid with work
+            uint32_t ns = 0, np = 0;                 // score blocks and P V products issued
             auto commit = [&](int which) {
                 if (elect_one()) umma_commit(bar + which);
-                __syncwarp();
-            };
-            auto scores = [&](int t, uint32_t s) {
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = (ks >> 2) * 1024 + (ks & 3) * 2;
-                        umma_bf16(tmem + t * 128, dq + (t * STEP + o), dk + (s * STEP + o), id_s, ks > 0);
-                    }
-                    umma_commit(bar + S_FULL + t);
-                }
                 __syncwarp();
             };
             bool ok = true, more = true;
             while (more) {
                 const Work w(a, bx, by, bz);
                 if (w.i0 < w.n) {
-                    const Visits v0(a, w.i0, w.n), v1(a, w.i0 + 128, w.n);
+                    const Visits v(a, w.i0 + t * 128, w.n);
                     const KeyTiles kt = w.tiles(a);
-                    const int nt = kt.count();
-                    uint32_t acc[2] = {0, 0};
-                    ok = mbar_wait(bar + Q_FULL, qph, a.err) && mbar_wait(bar + K_FULL + (kc & 1), (kc >> 1) & 1, a.err);
-                    ok = __all_sync(~0u, ok);
+                    const int nu = 2 * kt.count();
+                    uint32_t acc = 0;
+                    ok = __all_sync(~0u, mbar_wait(bar + Q_FULL, qph, a.err));
                     qph ^= 1;
-                    if (ok) {
-                        tc_fence_after();
-                        if (v0(kt.tile(0))) scores(0, kc & 1);
-                        if (v1(kt.tile(0))) scores(1, kc & 1);
-                        commit(K_EMPTY + (kc & 1));
-                        if (nt == 1) commit(Q_EMPTY);
-                    }
-                    for (int c = 0; ok && c < nt; ++c, ++kc) {
-                        const uint32_t s = kc & 1, ph = (kc >> 1) & 1;
-                        const int j = kt.tile(c), jn = c + 1 < nt ? kt.tile(c + 1) : -1;
-                        ok = mbar_wait(bar + V_FULL + s, ph, a.err);
-                        if (ok && jn >= 0) ok = mbar_wait(bar + K_FULL + (s ^ 1), ((kc + 1) >> 1) & 1, a.err);
-                        ok = __all_sync(~0u, ok);
+                    for (int u = 0; ok && u <= nu; ++u) {
+                        const uint32_t hf = u & 1;
+                        if (u < nu) {  // scores of block u
+                            const uint32_t s = kc & 1;
+                            if (!hf) ok = __all_sync(~0u, mbar_wait(bar + K_FULL + s, (kc >> 1) & 1, a.err));
+                            if (!ok) break;
+                            if (v(kt.tile(u >> 1) * 2 + hf)) {
+                                // (over P of the block before last, whose product was issued
+                                // before: products run in order)
+                                tc_fence_after();
+                                if (elect_one()) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const Visits &v = t ? v1 : v0;
-                            if (ok && v(j)) {
-                                ok = __all_sync(~0u, mbar_wait(bar + P_FULL + t, pph[t], a.err));
-                                pph[t] ^= 1;
+                                    for (int ks = 0; ks < D / 16; ++ks) {
+                                        const uint32_t o = (ks >> 2) * 1024 + (ks & 3) * 2;
+                                        umma_bf16(ts + (ns & 1) * 64, dq + o, dk + (s * STEP + hf * 512 + o), id_s, ks > 0);
+                                    }
+                                    umma_commit(bar + S_FULL + 2 * t + (ns & 1));
+                                }
+                                __syncwarp();
+                                ++ns;
+                            }
+                            if (hf) {
+                                commit(K_EMPTY + s);
+                                ++kc;
+                            }
+                            if (u == nu - 1) commit(Q_EMPTY);
+                        }
+                        if (u > 0) {   // outputs of block u - 1
+                            const uint32_t s = vc & 1, bf = np & 1;
+                            const int j = kt.tile((u - 1) >> 1) * 2 + (hf ^ 1);
+                            if (hf) ok = mbar_wait(bar + V_FULL + s, (vc >> 1) & 1, a.err);
+                            if (v(j)) {
+                                ok = ok && mbar_wait(bar + P_FULL + 2 * t + bf, (np >> 1) & 1, a.err);
+                                ok = __all_sync(~0u, ok);
                                 tc_fence_after();
                                 if (ok && elect_one()) {
 #pragma unroll
-                                    for (int ks = 0; ks < 8; ++ks)
-                                        umma_bf16_ts(tmem + L::TM_O + t * D, tmem + t * 128 + ks * 8,
-                                                     dv + (s * STEP + ks * 128), id_o, acc[t] | (ks > 0));
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        umma_bf16_ts(to, ts + bf * 64 + ks * 8, dv + (s * STEP + (hf ^ 1) * 512 + ks * 128), id_o,
+                                                     acc | (ks > 0));
+                                    umma_commit(bar + O_DONE + t);
                                     if (j == v.last) umma_commit(bar + O_LAST + t);
                                 }
                                 __syncwarp();
-                                acc[t] = 1;
+                                acc = 1;
+                                ++np;
                             }
-                            // (over P, which the product just issued reads: products run in order)
-                            if (ok && jn >= 0 && v(jn)) scores(t, s ^ 1);
+                            ok = __all_sync(~0u, ok);
+                            if (!ok) break;
+                            if (!hf) {
+                                commit(V_EMPTY + s);
+                                ++vc;
+                            }
                         }
-                        if (!ok) break;
-                        commit(V_EMPTY + s);
-                        if (jn >= 0) commit(K_EMPTY + (s ^ 1));
-                        if (c + 2 == nt) commit(Q_EMPTY);
                     }
                 }
                 more = advance(ok);
             }
-            commit(DRAINED);  // no product is in flight when the tensor memory is freed
-            mbar_wait(bar + DRAINED, 0, a.err);
+            commit(DRAINED + t);  // no product is in flight when the tensor memory is freed
+            mbar_wait(bar + DRAINED + t, 0, a.err);
         }
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
@@ -274,77 +300,94 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = lane_base + L::TM_O + t * D;
         const float sc = a.scale * kLog2E;
-        uint32_t sph = 0, lph = 0;
+        uint32_t ns = 0, lph = 0;  // blocks of scores this tile has taken, phase of O_LAST
         bool ok = true, more = true;
         while (more) {
             const Work w(a, bx, by, bz);
-            const int row = w.i0 + t * 128 + r, p = a.Tk - a.T + row, p0 = p - r;
+            const int row = w.i0 + t * 128 + r, p = a.Tk - a.T + row;
             float m = -INFINITY, l = 0.f;
             bool started = false;
             if (w.i0 < w.n) {
                 const Visits visits(a, w.i0 + t * 128, w.n);
                 const KeyTiles kt = w.tiles(a);
-                const int nt = kt.count();
-                for (int c = 0; c < nt; ++c) {
-                    const int j = kt.tile(c), j0 = j * 128;
+                const int nu = 2 * kt.count();
+                for (int u = 0; u < nu; ++u) {
+                    const int j = kt.tile(u >> 1) * 2 + (u & 1);
                     if (!visits(j)) continue;
-                    const uint32_t ts = lane_base + t * 128;
-                    ok = __all_sync(~0u, mbar_wait(bar + S_FULL + t, sph, a.err));
+                    const uint32_t bf = ns & 1, ts = lane_base + t * 128 + bf * 64;
+                    ok = __all_sync(~0u, mbar_wait(bar + S_FULL + 2 * t + bf, (ns >> 1) & 1, a.err));
                     if (!ok) break;
-                    sph ^= 1;
                     tc_fence_after();
-                    float s[128];
+                    float s[64], sum[4];
+                    uint32_t v[32];
+                    auto take_scores = [&] {
+                        tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(s));
+                        tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+                        tmem_ld_wait(s);
+                    };
+                    auto exponentials = [&](float ms) {
+                        sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 128; x += 32) tmem_ld32(ts + x, *reinterpret_cast<float(*)[32]>(s + x));
-                    tmem_ld_wait(s);
-                    if (!tile_full(p0, p0 + 127, j0, j0 + 128, a.window, a.sinks)) {
-                        const int hi = p - j0, lo = p - a.window + 1 - j0, sk = a.sinks - j0;
-#pragma unroll
-                        for (int x = 0; x < 128; ++x) s[x] = x <= hi && (x >= lo || x < sk) ? s[x] : -INFINITY;
-                    }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int x = 4; x < 128; x += 4)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[x + y]);
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    const bool grow = mt > m + kMaxGrowth;  // also the first finite score of the row
-                    if (__any_sync(~0u, grow)) {
-                        const float f = grow ? ex2_approx(m - mt) : 1.f;
-                        if (grow) m = mt;
-                        l *= f;
-                        if (started) {  // there is an O to rescale
-                            for (int x = 0; x < D; x += 16) {
-                                float o[16];
-                                tmem_ld16(to + x, o);
-                                tmem_ld_wait(o);
-                                uint32_t v[16];
-#pragma unroll
-                                for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * f);
-                                tmem_st16(to + x, v);
-                            }
-                        }
-                    }
-                    started = true;
-                    const float ms = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {};
-#pragma unroll
-                    for (int x0 = 0; x0 < 128; x0 += 64) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int x = x0; x < x0 + 64; x += 2) {
+                        for (int x = 0; x < 64; x += 2) {
                             const float e0 = ex2_approx(fmaf(s[x], sc, -ms)), e1 = ex2_approx(fmaf(s[x + 1], sc, -ms));
                             sum[x & 2] += e0;
                             sum[(x & 2) + 1] += e1;
                             const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
-                            v[(x - x0) / 2] = *reinterpret_cast<const uint32_t *>(&e);
+                            v[x / 2] = *reinterpret_cast<const uint32_t *>(&e);
                         }
-                        tmem_st32(ts + x0 / 2, v);
+                    };
+                    const bool full = visits.full(j);
+                    bool careful = !full || __any_sync(~0u, m == -INFINITY);
+                    take_scores();
+                    if (__builtin_expect(!careful, 1)) {
+                        exponentials(m);
+                        careful = __any_sync(~0u, !((sum[0] + sum[1]) + (sum[2] + sum[3]) < kMaxSum));
+                        if (__builtin_expect(careful, 0)) take_scores();
                     }
+                    if (__builtin_expect(careful, 0)) {
+                        if (!full) {
+                            const int j0 = j * 64, hi = p - j0, lo = p - a.window + 1 - j0, sk = a.sinks - j0;
+#pragma unroll
+                            for (int x = 0; x < 64; ++x) s[x] = x <= hi && (x >= lo || x < sk) ? s[x] : -INFINITY;
+                        }
+                        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int x = 4; x < 64; x += 4)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[x + y]);
+                        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                        const bool grow = mt > m + kMaxGrowth;  // also the first finite score of the row
+                        if (__any_sync(~0u, grow)) {
+                            const float f = grow ? ex2_approx(m - mt) : 1.f;
+                            if (grow) m = mt;
+                            l *= f;
+                            if (started) {
+                                // rescale O, once the product before this block is in it.  (The one
+                                // before that was complete when these scores were, so the parity is
+                                // unambiguous.)
+                                ok = __all_sync(~0u, mbar_wait(bar + O_DONE + t, (ns - 1) & 1, a.err));
+                                if (!ok) break;
+                                tc_fence_after();
+                                for (int x = 0; x < D; x += 16) {
+                                    float o[16];
+                                    tmem_ld16(to + x, o);
+                                    tmem_ld_wait(o);
+                                    uint32_t g[16];
+#pragma unroll
+                                    for (int y = 0; y < 16; ++y) g[y] = __float_as_uint(o[y] * f);
+                                    tmem_st16(to + x, g);
+                                }
+                            }
+                        }
+                        exponentials(m == -INFINITY ? 0.f : m);
+                    }
+                    started = true;
+                    tmem_st32(ts, v);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar + P_FULL + t);
+                    if (lane == 0) mbar_arrive(bar + P_FULL + 2 * t + bf);
+                    ++ns;
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
             }
