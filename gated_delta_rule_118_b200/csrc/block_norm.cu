@@ -523,8 +523,7 @@ cudaError_t bwd_impl(const NormArgs &a, int num_sms, cudaStream_t stream)
     const NormPlan p = plan_bwd(a.N, a.D, num_sms, sizeof(E));
     const cudaError_t e = a.D % 8 == 0 ? bwd_rows<E, true>(a, p, stream) : bwd_rows<E, false>(a, p, stream);
     if (e != cudaSuccess) return e;
-    norm_reduce_kernel<<<(a.D + 31) / 32, 1024, 0, stream>>>(a, p.rows);
-    return cudaGetLastError();
+    return launch_plain(norm_reduce_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, stream, a, p.rows);
 }
 
 }  // namespace

@@ -165,6 +165,19 @@ cudaError_t ensure_smem_limit(Kernel kern, int bytes, std::atomic<unsigned long 
     return e;
 }
 
+// A plain launch.  The status is this launch's own: the runtime's last error, which a
+// triple-bracket launch would be asked for, may be left from somebody else's call.
+template <typename... P, typename... A>
+cudaError_t launch_plain(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Launch configuration with the programmatic-dependent-launch attribute set when `overlap`.
 struct LaunchCfg {
     cudaLaunchConfig_t cfg{};

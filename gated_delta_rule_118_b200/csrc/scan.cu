@@ -457,15 +457,12 @@ cudaError_t launch_scan_step(const ScanArgs &a, float *h, bool bf16, cudaStream_
 {
     const long long n = (long long)a.B * a.C, per = n % 4 == 0 ? 1024 : 256, blocks = (n + per - 1) / per;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks;
-    if (n % 4 == 0) {
-        if (bf16) scan_step4_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, h);
-        else scan_step4_kernel<float><<<grid, 256, 0, stream>>>(a, h);
-    } else {
-        if (bf16) scan_step_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, h);
-        else scan_step_kernel<float><<<grid, 256, 0, stream>>>(a, h);
-    }
-    return cudaGetLastError();
+    const dim3 grid((unsigned)blocks), block(256);
+    if (n % 4 == 0)
+        return bf16 ? launch_plain(scan_step4_kernel<__nv_bfloat16>, grid, block, 0, stream, a, h)
+                    : launch_plain(scan_step4_kernel<float>, grid, block, 0, stream, a, h);
+    return bf16 ? launch_plain(scan_step_kernel<__nv_bfloat16>, grid, block, 0, stream, a, h)
+                : launch_plain(scan_step_kernel<float>, grid, block, 0, stream, a, h);
 }
 
 }  // namespace gdn2

@@ -659,14 +659,12 @@ cudaError_t impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream
         !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128) || !make_rows_map(&mg, a.dO, D, a.Hq, a.T, a.B, gs, 128))
         return cudaErrorInvalidValue;
     const int items = plan.nseg ? plan.nsink * plan.nseg + plan.ntiles - plan.nsink : plan.ntiles;
-    dkdv_tc_kernel<D><<<dim3(a.Hk, a.B, items), kThreads, KvLayout<D>::BYTES, stream>>>(a, plan, mq, mk, mv, mg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    dq_tc_kernel<D><<<dim3(a.Hq, a.B, (a.T + 127) / 128), kThreads, QLayout<D>::BYTES, stream>>>(a, mq, mk, mv, mg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (plan.nseg && plan.nsink) {
-        sink_sum_kernel<D><<<dim3(plan.nsink * 16, a.Hk, a.B), 256, 0, stream>>>(a, plan);
-        e = cudaGetLastError();
-    }
+    e = launch_plain(dkdv_tc_kernel<D>, dim3(a.Hk, a.B, items), dim3(kThreads), KvLayout<D>::BYTES, stream, a, plan, mq, mk, mv, mg);
+    if (e == cudaSuccess)
+        e = launch_plain(dq_tc_kernel<D>, dim3(a.Hq, a.B, (a.T + 127) / 128), dim3(kThreads), QLayout<D>::BYTES, stream, a, mq, mk,
+                         mv, mg);
+    if (e == cudaSuccess && plan.nseg && plan.nsink)
+        e = launch_plain(sink_sum_kernel<D>, dim3(plan.nsink * 16, a.Hk, a.B), dim3(256), 0, stream, a, plan);
     return e;
 }
 

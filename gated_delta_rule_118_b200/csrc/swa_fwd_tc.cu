@@ -453,8 +453,7 @@ cudaError_t impl(const SwaArgs &a, cudaStream_t stream)
     if (!make_rows_map(&mq, a.q, D, a.Hq, a.T, a.B, a.qs, 128) || !make_rows_map(&mk, a.k, D, a.Hk, a.Tk, a.B, a.ks, 128) ||
         !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128))
         return cudaErrorInvalidValue;
-    kern<<<dim3(a.Hq, a.B, (a.T + 255) / 256), kThreads, L::BYTES, stream>>>(a, mq, mk, mv);
-    return cudaGetLastError();
+    return launch_plain(kern, dim3(a.Hq, a.B, (a.T + 255) / 256), dim3(kThreads), L::BYTES, stream, a, mq, mk, mv);
 }
 
 }  // namespace

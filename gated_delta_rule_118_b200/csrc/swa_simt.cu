@@ -3,6 +3,7 @@
 // tiles).  The products are 64-wide register tiles over shared memory; bound by
 // the FFMA rate (every score costs 2 d FMAs, and the two-kernel backward forms
 // q k^T and dO v^T twice in exchange for a fixed order of every sum).
+#include "launch.h"
 #include "swa_common.cuh"
 
 namespace gdn2 {
@@ -397,30 +398,29 @@ template <typename E, int D>
 cudaError_t fwd_impl(const SwaArgs &a, cudaStream_t stream)
 {
     constexpr int bytes = sizeof(float) * (2 * 64 * (D + 4) + 64 * 68);
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<unsigned long long> set{0};
+    const cudaError_t e = ensure_smem_limit(fwd_kernel<E, D>, bytes, set);
     if (e != cudaSuccess) return e;
-    fwd_kernel<E, D><<<dim3((a.T + 63) / 64, a.Hq, a.B), kThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_plain(fwd_kernel<E, D>, dim3((a.T + 63) / 64, a.Hq, a.B), dim3(kThreads), bytes, stream, a);
 }
 
 template <typename E, int D>
 cudaError_t bwd_impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
 {
     constexpr int dq_bytes = sizeof(float) * (192 * (D + 4) + 64 * 36), kv_bytes = sizeof(float) * (192 * (D + 4) + 32 * 68);
-    cudaError_t e = cudaFuncSetAttribute(dq_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_bytes);
+    static std::atomic<unsigned long long> dq_set{0}, kv_set{0};
+    cudaError_t e = ensure_smem_limit(dq_kernel<E, D>, dq_bytes, dq_set);
+    if (e == cudaSuccess) e = ensure_smem_limit(dkdv_kernel<E, D>, kv_bytes, kv_set);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dkdv_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
-    if (e != cudaSuccess) return e;
-    dq_kernel<E, D><<<dim3((a.T + 63) / 64, a.Hq, a.B), kThreads, dq_bytes, stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+        e = launch_plain(dq_kernel<E, D>, dim3((a.T + 63) / 64, a.Hq, a.B), dim3(kThreads), dq_bytes, stream, a);
     const int nsplit = kv_split(a, num_sms);
-    dkdv_kernel<E, D><<<dim3((a.Tk + 63) / 64 * nsplit, a.Hk, a.B), kThreads, kv_bytes, stream>>>(a, nsplit, part);
-    e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = launch_plain(dkdv_kernel<E, D>, dim3((a.Tk + 63) / 64 * nsplit, a.Hk, a.B), dim3(kThreads), kv_bytes, stream, a, nsplit,
+                         part);
     if (e != cudaSuccess || nsplit == 1) return e;
     const long long keys = (long long)a.B * a.Hk * a.Tk;
-    dkdv_sum_kernel<E, D><<<(unsigned)((keys + 7) / 8), kThreads, 0, stream>>>(a, nsplit, part);
-    return cudaGetLastError();
+    return launch_plain(dkdv_sum_kernel<E, D>, dim3((unsigned)((keys + 7) / 8)), dim3(kThreads), 0, stream, a, nsplit,
+                        (const float *)part);
 }
 
 template <typename E, int D>
@@ -428,8 +428,7 @@ cudaError_t delta_impl(const SwaArgs &a, cudaStream_t stream)
 {
     const long long rows = (long long)a.B * a.T * a.Hq, blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    delta_kernel<E, D><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_plain(delta_kernel<E, D>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
