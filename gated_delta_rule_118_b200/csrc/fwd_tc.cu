@@ -73,9 +73,15 @@ cudaMemPool_t workspace_pool(int dev)
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         cudaMemPool_t p = nullptr;
-        if (cudaMemPoolCreate(&p, &props) != cudaSuccess) return nullptr;
+        // (the first call on a device may be one that a graph captures: creating a pool is no
+        // work of a stream, but a capture in its default mode would be invalidated by it)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+        const cudaError_t created = cudaMemPoolCreate(&p, &props);
         uint64_t keep = ~0ull;
-        cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (created == cudaSuccess) cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (created != cudaSuccess) return nullptr;
         pools[dev] = p;
     }
     return pools[dev];

@@ -1,6 +1,10 @@
 """The hybrid block's operators used together: block norms around a gated delta
 rule layer, a window-attention layer and a gated linear recurrence; prefill then
 decode, and a training step whose gradients are checked against autograd in fp64."""
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -120,3 +124,83 @@ def test_training_step_gradients():
     got = [b1["dr"], ba["dq"], ba["dk"], ba["dv"], b1["dg_logit"], bs["dw"], bs["dlog_alpha"]]
     for name, a, b in zip(leaves, got, ref):
         assert (a.double() - b).norm() <= 2e-5 * b.norm(), (name, (a.double() - b).norm() / b.norm())
+
+
+FIRST_CALL = """
+import torch
+import gated_delta_rule_118_b200 as g
+x = torch.randn(2, 300, 128, device="cuda")
+v = torch.ones(128, device="cuda")
+q = torch.randn(1, 300, 2, 128, device="cuda").bfloat16()
+calls = dict(swa_fwd=lambda: g.gdn2_swa_fwd(q, q, q, window=64, sinks=2)[0],
+             swa_bwd=lambda: g.gdn2_swa_bwd(q, q, q, q, torch.zeros(1, 2, 300, device="cuda"), q, window=64)["dq"],
+             scan=lambda: g.gdn2_scan_fwd(x, x, -x.abs())[0],
+             norm_bwd=lambda: g.gdn2_block_norm_bwd(x, x, x, v, v, v, x, x)["dr"])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = calls["%s"]()
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, calls["%s"]())
+"""
+
+
+@pytest.mark.parametrize("call", ["swa_fwd", "swa_bwd", "scan", "norm_bwd"])
+def test_the_first_call_of_a_process_can_be_captured(call):
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % (call, call)], cwd=Path(__file__).resolve().parents[1],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_graphs_with_workspaces_replayed_on_two_streams():
+    """Graphs of calls that take workspaces, replayed at the same time, do not share them."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    f = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    sets = []
+    for _ in range(2):
+        q, k, v, dO = (f(1, 900, 4, 64).bfloat16() for _ in range(4))
+        o, lse = g.gdn2_swa_fwd(q, k, v, window=100, sinks=3)
+        args = (f(400, 256), f(400, 256), f(400, 256), f(256), f(256), f(256), f(400, 256), f(400, 256))
+        both = lambda q=q, k=k, v=v, o=o, lse=lse, dO=dO, args=args: (  # noqa: E731
+            *g.gdn2_swa_bwd(q, k, v, o, lse, dO, window=100, sinks=3).values(), *g.gdn2_block_norm_bwd(*args).values())
+        ref = both()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = both()
+        sets.append((graph, got, ref, both))  # (the inputs stay alive with their graph)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (graph, *_) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, ref, _ in sets:
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_calls_from_two_threads():
+    import threading
+    gen = torch.Generator("cuda").manual_seed(4)
+    q, k, v, dO = (torch.randn(1, 700, 4, 128, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    kw = dict(window=90, sinks=2)
+    o, lse = g.gdn2_swa_fwd(q, k, v, **kw)
+    ref = [o, *g.gdn2_swa_bwd(q, k, v, o, lse, dO, **kw).values()]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                o, lse = g.gdn2_swa_fwd(q, k, v, **kw)
+                got = [o, *g.gdn2_swa_bwd(q, k, v, o, lse, dO, **kw).values()]
+                torch.cuda.current_stream().synchronize()
+                bad.extend(i for i, (a, b) in enumerate(zip(got, ref)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
