@@ -37,18 +37,31 @@ constexpr int kSpan = kWarps * kTok;      // tokens of a CTA
 constexpr int kChan = 64;                 // channels of a CTA
 constexpr int kMaxCluster = 8;
 
-// The pair of channels c, c + 1 of a row; 0 (or `fill`) outside [0, C).
+// The pair of channels c, c + 1 of a row; 0 outside [0, C).
 template <bool EVEN, typename E>
-__device__ __forceinline__ f2 load_pair(const E *row, int c, int C, float fill = 0.f)
+__device__ __forceinline__ f2 load_pair(const E *row, int c, int C)
 {
     if constexpr (EVEN) {
-        if (c >= C) return both(fill);
+        if (c >= C) return 0;
         alignas(8) E e[2];
         if constexpr (sizeof(E) == 4) *reinterpret_cast<float2 *>(e) = __ldg(reinterpret_cast<const float2 *>(row + c));
         else *reinterpret_cast<uint32_t *>(e) = __ldg(reinterpret_cast<const uint32_t *>(row + c));
         return pair_of(e);
     } else {
-        return pack2(c < C ? to_f32(row[c]) : fill, c + 1 < C ? to_f32(row[c + 1]) : fill);
+        return pack2(c < C ? to_f32(row[c]) : 0.f, c + 1 < C ? to_f32(row[c + 1]) : 0.f);
+    }
+}
+// The pair of a state that the kernel's own result may overwrite (not through the read-only
+// path, whose loads may be moved over a barrier).
+template <bool EVEN>
+__device__ __forceinline__ f2 load_state(const float *row, int c, int C)
+{
+    if constexpr (EVEN) {
+        if (c >= C) return 0;
+        const float2 v = *reinterpret_cast<const float2 *>(row + c);
+        return pack2(v.x, v.y);
+    } else {
+        return load_pair<EVEN>(row, c, C);
     }
 }
 template <bool EVEN, typename E>
@@ -171,7 +184,7 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
     const Place pl(csize);
     const int warp = threadIdx.x >> 5, c = pl.c, c_cta = (int)(blockIdx.x / csize) * kChan;
     const long long seq = (long long)pl.b * a.T, step = (long long)kSpan * pl.size;
-    const int nblk = (a.T + kTok - 1) / kTok;
+    const int nblk = (a.T - 1) / kTok + 1;
     if (SRC == kTile && threadIdx.x == 0) {
         for (int i = 0; i < S::COUNT; ++i) sm100::mbar_init(full + i, 1);
         sm100::fence_mbar_init();
@@ -182,7 +195,7 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         sm100::mbar_init(maps.landed + threadIdx.x, 1);
         sm100::fence_mbar_init();
     }
-    f2 state = a.h0 ? load_pair<EVEN>(a.h0 + (long long)pl.b * a.C, c, a.C) : 0;
+    f2 state = a.h0 ? load_state<EVEN>(a.h0 + (long long)pl.b * a.C, c, a.C) : 0;
     __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read h0, which h_T may alias)
     int k = 0, st = 0;
@@ -241,7 +254,7 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
     const Place pl(csize);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = pl.c, c_cta = (int)(blockIdx.x / csize) * kChan;
     const long long seq = (long long)pl.b * a.T, step = (long long)kSpan * pl.size, spans = (a.T + step - 1) / step;
-    const int nblk = (a.T + kTok - 1) / kTok;
+    const int nblk = (a.T - 1) / kTok + 1;
     // along the walk the last tokens come first: rank 0 and warp 0 take the latest
     auto first_token = [&](long long sp) { return sp * step + (pl.size - 1 - pl.rank) * kSpan; };
     if (SRC == kTile && threadIdx.x == 0) {
@@ -257,7 +270,7 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         sm100::mbar_init(maps.landed + threadIdx.x, 1);
         sm100::fence_mbar_init();
     }
-    f2 state = a.dh_T ? load_pair<EVEN>(a.dh_T + (long long)pl.b * a.C, c, a.C) : 0;
+    f2 state = a.dh_T ? load_state<EVEN>(a.dh_T + (long long)pl.b * a.C, c, a.C) : 0;
     __syncthreads();
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read dh_T, which dh0 may alias)
     int k = 0, st = 0;

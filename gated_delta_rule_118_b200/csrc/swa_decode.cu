@@ -465,9 +465,8 @@ cudaError_t launch(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
     cudaError_t e = ensure_smem_limit(kern, bytes, set);
     if (e != cudaSuccess) return e;
     const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc, nsplit = splits(a, gc, PER_SM, num_sms);
-    if ((long long)a.Hk * nchunk > 65535) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);
+    cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);  // (y is at most the number of query heads)
     cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;

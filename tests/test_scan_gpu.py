@@ -79,6 +79,18 @@ def test_pieces_equal_the_whole_and_steps_continue(dtype):
     close(h, ref["h_T"], tol["h_T"], "h")
 
 
+@pytest.mark.parametrize("C", [64, 130, 65])
+def test_state_in_place_where_ctas_share_a_sequence(C):
+    """Every CTA of a cluster starts from h0, which one of them overwrites with h_T."""
+    x, w, la, h0, dy, dh = make(1, 700, C, F32, seed=6)
+    la.mul_(1e-3)  # (h0 is still there at the end)
+    y, h_T = g.gdn2_scan_fwd(x, w, la, h0)
+    for _ in range(50):
+        h = h0.clone()
+        again, _ = g.gdn2_scan_fwd(x, w, la, h, h_T=h)
+        assert torch.equal(h, h_T) and torch.equal(again, y)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("B,C", [(1, 1), (3, 5), (256, 2048), (7, 1001)])
 def test_step(B, C, dtype):
