@@ -58,13 +58,16 @@ __device__ __forceinline__ void issue_rows(uint32_t tm, uint64_t da, uint64_t db
     }
 }
 // D[128 x d] += A B: A bf16 in tensor memory (128 columns, 64 of them from tm_a, 64 from
-// tm_a + 64), B a tile of 128 rows of d.
-template <int D>
+// tm_a + 64), B a tile of 128 rows of d.  PAIR: A is a sum of two such matrices, the
+// second 32 columns behind the first.
+template <int D, bool PAIR>
 __device__ __forceinline__ void issue_cols(uint32_t tm, uint32_t tm_a, uint64_t db, uint32_t acc)
 {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        umma_bf16_ts(tm, tm_a + (ks >> 2) * 64 + (ks & 3) * 8, db + ks * 128, idesc_bf16(128, D, 0, 1), acc | (ks > 0));
+    for (int x = 0; x <= (int)PAIR; ++x)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+            umma_bf16_ts(tm, tm_a + x * 32 + (ks >> 2) * 64 + (ks & 3) * 8, db + ks * 128, idesc_bf16(128, D, 0, 1), acc | (x + ks > 0));
 }
 
 // 64 values packed to bf16 over the columns they came from.
@@ -77,6 +80,29 @@ __device__ __forceinline__ void put_bf16(uint32_t tm, const float (&f)[64])
         u[x / 2] = *reinterpret_cast<const uint32_t *>(&e);
     }
     tmem_st32(tm, u);
+    tmem_st_wait();
+    tc_fence_before();
+}
+
+// The same as a sum of two: the upper half of each value's bits (cut off, which takes no
+// conversion), and 32 columns behind what that leaves, rounded.  Together they carry 16
+// bits.
+__device__ __forceinline__ void put_bf16_pair(uint32_t tm, const float (&f)[64])
+{
+#pragma unroll
+    for (int y = 0; y < 64; y += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+            const uint32_t a = __float_as_uint(f[y + x]), b = __float_as_uint(f[y + x + 1]);
+            hi[x / 2] = __byte_perm(a, b, 0x7632);
+            const __nv_bfloat162 r = __floats2bfloat162_rn(f[y + x] - __uint_as_float(a & 0xffff0000u),
+                                                           f[y + x + 1] - __uint_as_float(b & 0xffff0000u));
+            lo[x / 2] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+        tmem_st16(tm + y / 2, hi);
+        tmem_st16(tm + 32 + y / 2, lo);
+    }
     tmem_st_wait();
     tc_fence_before();
 }
@@ -291,7 +317,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_cols<D>(tmem + L::TM_DV, tmem + L::TM_S, gt + s * STEP, i > 0);
+                    issue_cols<D, false>(tmem + L::TM_DV, tmem + L::TM_S, gt + s * STEP, i > 0);
                     if (next) scores(sn);  // over P^T, which the product just issued reads: products run in order
                 }
                 __syncwarp();
@@ -299,7 +325,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_cols<D>(tmem + L::TM_DK, tmem + L::TM_DP, qt + s * STEP, i > 0);
+                    issue_cols<D, true>(tmem + L::TM_DK, tmem + L::TM_DP, qt + s * STEP, i > 0);
                     umma_commit(bar + QG_EMPTY + s);
                     if (next) dots(sn);
                 }
@@ -357,7 +383,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
             }
 #pragma unroll
             for (int x = 0; x < 64; ++x) g[x] *= p[x];
-            put_bf16(tp, g);
+            put_bf16_pair(tp, g);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + DS_FULL);
         }
@@ -545,7 +571,7 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_cols<D>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + kd * STEP, c > 0);
+                    issue_cols<D, true>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + kd * STEP, c > 0);
                     umma_commit(bar + K_EMPTY + kd);
                 }
                 __syncwarp();
@@ -599,7 +625,7 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
 #pragma unroll
                 for (int x = 0; x < 64; ++x) g[x] = p[x] == 0.f ? 0.f : g[x];
             }
-            put_bf16(tp, g);
+            put_bf16_pair(tp, g);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + DSQ_FULL + s);
         }
