@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(256) sink_sum_kernel(const __grid_constant__ S
 
 // ---------------------------------------------------------------- dq
 enum { QD_FULL, K_FULL, K_EMPTY = K_FULL + 3, V_FULL = K_EMPTY + 3, V_EMPTY, SQ_FULL, SQ_FREE,
-       DPQ_FULL, DSQ_FULL = DPQ_FULL + 2, DONE_Q = DSQ_FULL + 2, NBAR_Q };
+       DPQ_FULL, DSQ_FULL = DPQ_FULL + 2, DQ_DONE = DSQ_FULL + 2, SCORES_DONE = DQ_DONE + 2, DONE_Q, NBAR_Q };
 
 template <int D>
 struct QLayout {
@@ -533,26 +533,27 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
         } else if (warp == kMma) {
             const uint64_t dq = smem_desc(sbase + L::Q, 16, 1024, kSw128), dg = smem_desc(sbase + L::G, 16, 1024, kSw128);
             const uint64_t dk = smem_desc(sbase + L::K, 16, 1024, kSw128), dv = smem_desc(sbase + L::V, 16, 1024, kSw128);
-            const uint64_t kt_ = smem_desc(sbase + L::K, 16384, 1024, kSw128);
             constexpr uint32_t STEP = Tiles<D>::STEP;
-            bool ok = mbar_wait(bar + QD_FULL, 0, a.err);
-            // S and dP of tile c; S goes over the S that has been read, dP into the buffer whose
-            // dS was the operand of a product issued before
-            uint32_t ks = 0, kph = 0;  // K stage of the next scores
-            auto scores = [&](int c) {
+            bool ok = __all_sync(~0u, mbar_wait(bar + QD_FULL, 0, a.err));
+            uint32_t ks = 0, kph = 0;  // K stage
+            for (int c = 0; ok && c < N; ++c) {
+                // S and dP of tile c; S goes over the S that has been read, dP over dS of the tile
+                // before last, which its product has read
                 const uint32_t s = c & 1;
-                ok = ok && mbar_wait(bar + K_FULL + ks, kph, a.err);
-                if (c > 0) ok = ok && mbar_wait(bar + SQ_FREE, (c - 1) & 1, a.err);
+                ok = mbar_wait(bar + K_FULL + ks, kph, a.err);
+                if (c > 0) ok = ok && mbar_wait(bar + SQ_FREE, s ^ 1, a.err);
                 ok = __all_sync(~0u, ok);
-                if (!ok) return;
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
                     issue_rows<D>(tmem + L::TM_S, dq, dk + ks * STEP);
                     umma_commit(bar + SQ_FULL);
                 }
                 __syncwarp();
-                ok = __all_sync(~0u, mbar_wait(bar + V_FULL, s, a.err));
-                if (!ok) return;
+                ok = mbar_wait(bar + V_FULL, s, a.err);
+                if (c > 1) ok = ok && mbar_wait(bar + DQ_DONE + s, ((c >> 1) & 1) ^ 1, a.err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
                     issue_rows<D>(tmem + L::TM_DP + s * 128, dg, dv);
@@ -561,25 +562,33 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
                 }
                 __syncwarp();
                 if (++ks == 3) ks = 0, kph ^= 1;
-            };
-            scores(0);
-            uint32_t kd = 0;           // K stage of the next dQ
-            for (int c = 0; ok && c < N; ++c) {
+            }
+            if (elect_one()) umma_commit(bar + SCORES_DONE);
+            __syncwarp();
+            mbar_wait(bar + SCORES_DONE, 0, a.err);  // no product is in flight when the tensor memory is freed
+        } else if (warp == kRows) {
+            // the products of dQ from a warp of their own: issuing takes about as long as their
+            // work, and the next scores would wait for it
+            const uint64_t dk = smem_desc(sbase + L::K, 16384, 1024, kSw128);
+            bool ok = true;
+            uint32_t ks = 0, kph = 0;
+            for (int c = 0; c < N; ++c) {
                 const uint32_t s = c & 1;
-                if (c + 1 < N) scores(c + 1);
-                ok = __all_sync(~0u, ok && mbar_wait(bar + DSQ_FULL + s, (c >> 1) & 1, a.err));
+                ok = mbar_wait(bar + K_FULL + ks, kph, a.err) && mbar_wait(bar + DSQ_FULL + s, (c >> 1) & 1, a.err);
+                ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_cols<D, true>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, kt_ + kd * STEP, c > 0);
-                    umma_commit(bar + K_EMPTY + kd);
+                    issue_cols<D, true>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, dk + ks * Tiles<D>::STEP, c > 0);
+                    umma_commit(bar + DQ_DONE + s);
+                    umma_commit(bar + K_EMPTY + ks);
                 }
                 __syncwarp();
-                if (++kd == 3) kd = 0;
+                if (++ks == 3) ks = 0, kph ^= 1;
             }
             if (elect_one()) umma_commit(bar + DONE_Q);
             __syncwarp();
-            mbar_wait(bar + DONE_Q, 0, a.err);  // no product is in flight when the tensor memory is freed
+            mbar_wait(bar + DONE_Q, 0, a.err);
         }
     } else {
         setmaxnreg_inc<kRegsCompute>();
