@@ -377,21 +377,45 @@ int kv_split(const SwaArgs &a, int num_sms)
     return n;
 }
 
-// delta = dO . o of every row that holds a token, one warp per row.
+// delta = dO . o of every row that holds a token (0 in the others): 16 bytes a lane, so 8
+// to 32 lanes a row, and kDeltaRows rows a lane.  Bound by HBM.
+constexpr int kDeltaRows = 4;
+__device__ __forceinline__ long long quotient(long long n, int d)  // (64-bit division takes as long as the loads)
+{
+    return n < 0x7fffffffLL ? (unsigned)n / (unsigned)d : n / d;
+}
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) delta_kernel(const SwaArgs a)
 {
-    const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (b, t, h)
-    if (row >= (long long)a.B * a.T * a.Hq) return;
-    const int lane = threadIdx.x & 31, h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.T), b = (int)(row / a.Hq / a.T);
-    float s = 0.f;
-    if (t < seq_len(a, b)) {
-        const E *o = static_cast<const E *>(a.o) + row * D, *g = static_cast<const E *>(a.dO) + row * D;
+    constexpr int W = 16 / sizeof(E), LPR = D / W, RPC = kThreads / LPR;  // elements a lane, lanes a row, rows at a time
+    const long long rows = (long long)a.B * a.T * a.Hq, row0 = (long long)blockIdx.x * (RPC * kDeltaRows) + threadIdx.x / LPR;
+    const int x = threadIdx.x % LPR * W;
+    uint4 o[kDeltaRows], g[kDeltaRows];
+    bool live[kDeltaRows];
+    long long to[kDeltaRows];
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) s = fmaf(to_f32(o[lane + 32 * u]), to_f32(g[lane + 32 * u]), s);
-        s = warp_sum(s);
+    for (int u = 0; u < kDeltaRows; ++u) {
+        const long long row = row0 + u * RPC;  // (b, t, h)
+        const long long bt = quotient(row, a.Hq);
+        const int h = (int)(row - bt * a.Hq), b = (int)quotient(bt, a.T), t = (int)(bt - (long long)b * a.T);
+        live[u] = row < rows && t < seq_len(a, b);
+        to[u] = row < rows ? ((long long)b * a.Hq + h) * a.T + t : -1;
+        o[u] = g[u] = make_uint4(0, 0, 0, 0);
+        if (live[u]) {
+            o[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.o) + row * D + x);
+            g[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.dO) + row * D + x);
+        }
     }
-    if (lane == 0) a.delta[((long long)b * a.Hq + h) * a.T + t] = s;
+#pragma unroll
+    for (int u = 0; u < kDeltaRows; ++u) {
+        const E *p = reinterpret_cast<const E *>(&o[u]), *r = reinterpret_cast<const E *>(&g[u]);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) s = fmaf(to_f32(p[e]), to_f32(r[e]), s);
+#pragma unroll
+        for (int w = LPR / 2; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
+        if (x == 0 && to[u] >= 0) a.delta[to[u]] = live[u] ? s : 0.f;
+    }
 }
 
 template <typename E, int D>
@@ -426,7 +450,8 @@ cudaError_t bwd_impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t st
 template <typename E, int D>
 cudaError_t delta_impl(const SwaArgs &a, cudaStream_t stream)
 {
-    const long long rows = (long long)a.B * a.T * a.Hq, blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    constexpr int per = kThreads * 16 / (D * (int)sizeof(E)) * kDeltaRows;
+    const long long rows = (long long)a.B * a.T * a.Hq, blocks = (rows + per - 1) / per;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_plain(delta_kernel<E, D>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
 }
