@@ -6,13 +6,18 @@
 // memory -- one launch, no workspace.  Bound by HBM: the visible cache is read once for
 // all query heads of the group.
 //
-// bf16: warp-level matrix instructions over 16 heads x 16 keys.  Keys and values go from
-// memory straight into operand registers, 16 bytes a load: a dot product does not care in
-// which order its channels are taken, so a lane's 16 bytes of a key serve as two k-steps
-// of it (the query is loaded in the same order), and an output tile takes every eighth
-// channel so that a lane's 16 bytes of a value row feed eight tiles.  (The fifth-generation
-// tensor core would need the rows in shared memory first; a step of 16 keys is 64 warp
-// instructions here against 8 KB from memory, so it would not be used a tenth.)
+// bf16: warp-level matrix instructions over 16 heads x 16 keys (8 heads for groups of up
+// to 8).  Keys and values are fetched one or two steps ahead, 16 bytes a lane, into a place
+// of the lane's own in shared memory, and go from there into operand registers as they are:
+// a dot product does not care in which order its channels are taken, so a lane's 16 bytes
+// of a key serve as two k-steps of it (the query is loaded in the same order), and an
+// output tile takes every eighth channel so that a lane's 16 bytes of a value row feed
+// eight tiles.  (The fifth-generation tensor core would not be used a tenth: a step of 16
+// keys is 64 warp instructions here against 8 KB from memory.)
+// 256 sequences of 2052 positions, 16 query heads of 128 over 4: 216 us, 4.98 TB/s; over
+// 16: 755 us, 5.70 TB/s; one sequence: 11 us.  What is left of the first is the CTAs' own
+// beginning and end (position, query, first rows; join), about 10 us a wave: three CTAs of
+// an SM overlap it (with two, and twice the bytes in flight, 231 us).
 // fp32: one key row per half or whole warp on the CUDA cores.
 #include <cooperative_groups.h>
 
@@ -258,22 +263,39 @@ __device__ __forceinline__ uint32_t pair_bf16(float x, float y)
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16 *p)
+__device__ __forceinline__ void copy16(uint32_t smem, const void *p)
 {
-    uint4 v;  // (not through the read-only path: another CTA of the cluster may just have put the new token there)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy_group_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_groups_wait()  // all but the last N
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Keys and values on their way: AHEAD steps of 16 rows of each a warp, every 16 bytes in
+// the place of the lane that asked for them and will use them (so no barrier is needed).
+// The warps' results take the same room afterwards.
+template <int NW, int GC, int D, int AHEAD>
+struct MmaShared {
+    static constexpr int STEP = 16 * D * 2;  // bytes of 16 rows
+    union {
+        uint8_t ring[NW][2 * AHEAD][STEP];
+        Partials<NW, GC, D> part;
+    };
+    Joined<GC, D> joined;
+};
+
 // HR x 8 query heads of a CTA: both halves of the matrix instruction's rows, or one (whose
-// registers then let a third CTA onto the SM, and more loads into flight).
-template <int D, int HR, int NW>
-__global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 : 2) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
+// registers then let a third or fourth CTA onto the SM).  PER_SM CTAs on an SM.
+template <int D, int HR, int NW, int AHEAD, int PER_SM>
+__global__ void __launch_bounds__(NW * 32, PER_SM) decode_mma_kernel(const SwaDecodeArgs a, int nsplit, int nchunk)
 {
     using E = __nv_bfloat16;
     constexpr int kHeads = 8 * HR;
     constexpr int NC = D / 32;  // 16-byte chunks of a row per lane
-    using Shared = DecodeShared<NW, kHeads, D>;
+    using Shared = MmaShared<NW, kHeads, D, AHEAD>;
     extern __shared__ __align__(16) uint8_t dyn[];
     auto &part = reinterpret_cast<Shared *>(dyn)->part;
     auto &joined = reinterpret_cast<Shared *>(dyn)->joined;
@@ -314,34 +336,49 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 
         const int p = vis.position(t < t1 ? t : t1 - 1);
         return p == P ? fresh : cache + vis.slot(p) * cstep;
     };
-    uint4 kf[2][NC], vf[4][D / 64];
-    auto load_keys = [&](int t) {
+    const uint8_t *ring = &reinterpret_cast<Shared *>(dyn)->ring[warp][0][0] + lane * 16;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    auto fetch_keys = [&](int t, int slot) {
+        if (t < t1) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const E *p = row(kn, kc, t + gr + 8 * r) + c * 8;
+            for (int r = 0; r < 2; ++r) {
+                const E *p = row(kn, kc, t + gr + 8 * r) + c * 8;
 #pragma unroll
-            for (int j = 0; j < NC; ++j) kf[r][j] = load_stream(p + j * 32);
+                for (int j = 0; j < NC; ++j) copy16(ring_at + slot * Shared::STEP + (r * NC + j) * 512, p + j * 32);
+            }
         }
+        copy_group_end();
     };
-    auto load_values = [&](int t) {
+    auto fetch_values = [&](int t, int slot) {
+        if (t < t1) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const E *p = row(vn, vc, t + 2 * c + (r & 1) + (r >> 1) * 8) + gr * 8;
+            for (int r = 0; r < 4; ++r) {
+                const E *p = row(vn, vc, t + 2 * c + (r & 1) + (r >> 1) * 8) + gr * 8;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) vf[r][j] = load_stream(p + j * 64);
+                for (int j = 0; j < D / 64; ++j) copy16(ring_at + (AHEAD + slot) * Shared::STEP + (r * (D / 64) + j) * 512, p + j * 64);
+            }
         }
+        copy_group_end();
     };
+    auto at = [&](int slot, int n) { return *reinterpret_cast<const uint4 *>(ring + slot * Shared::STEP + n * 512); };
     float m[HR], l[HR] = {}, o[D / 8][2 * HR] = {};
 #pragma unroll
     for (int h = 0; h < HR; ++h) m[h] = -INFINITY;
     const float sc = a.scale * kLog2E;
     int t = t0 + warp * 16;
-    if (t < t1) {
-        load_keys(t);
-        load_values(t);
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+        fetch_keys(t + n * NW * 16, n);
+        fetch_values(t + n * NW * 16, n);
     }
-    for (; t < t1; t += NW * 16) {
+    for (int slot = 0; t < t1; t += NW * 16, slot = slot + 1 == AHEAD ? 0 : slot + 1) {
         float s[2][2 * HR] = {};
+        copy_groups_wait<2 * AHEAD - 1>();
+        uint4 kf[2][NC];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) kf[r][j] = at(slot, r * NC + j);
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -354,8 +391,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 
                     mma_bf16(s[r], q[0][j].z, q[0][j].w, kf[r][j].z, kf[r][j].w);
                 }
             }
-        const int tn = t + NW * 16;
-        if (tn < t1) load_keys(tn);
+        fetch_keys(t + AHEAD * NW * 16, slot);  // (behind the products, which have read the slot)
         // s[r][0..1]: head gr, keys 8 r + 2 c + {0, 1}; s[r][2..3]: head gr + 8
         float mx[HR];
         bool grow = false;
@@ -407,6 +443,12 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int h = 0; h < HR; ++h) p[r][h] = pair_bf16(s[r][2 * h], s[r][2 * h + 1]);
+        copy_groups_wait<2 * AHEAD - 1>();
+        uint4 vf[4][D / 64];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) vf[r][j] = at(AHEAD + slot, r * (D / 64) + j);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
             const uint32_t *w0 = &vf[0][j].x, *w1 = &vf[1][j].x, *w2 = &vf[2][j].x, *w3 = &vf[3][j].x;
@@ -418,8 +460,10 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 
                 else mma_bf16(o[j * 8 + n], p[0][0], p[1][0], b0, b1);
             }
         }
-        if (tn < t1) load_values(tn);
+        fetch_values(t + AHEAD * NW * 16, slot);
     }
+    copy_groups_wait<0>();
+    __syncthreads();  // the warps' results go over the rings
     // o[j * 8 + n][0..1]: head gr, channels 64 j + 8 (2 c + {0, 1}) + n; [2..3]: head gr + 8
 #pragma unroll
     for (int h = 0; h < HR; ++h) {
@@ -440,52 +484,66 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : HR == 1 && D == 64 ? 4 
     join<E, D, NW, kHeads>(part, joined, out, split, nsplit, ng);
 }
 
+// GC query heads of a group and NW warps per CTA.
+//
 // CTAs that share a (sequence, heads) row: the number with the least waves x time of a
-// CTA, whose own cost (query, join, cluster) counts as much as about 300 positions
-// (64 x 4 rows of 2052 positions of 128 bf16: 103 us split in 8, 78 in 4, 68 in 2).
-int splits(const SwaDecodeArgs &a, int gc, int per_sm, int num_sms)
+// CTA, whose own cost (query, join, cluster) counts as much as about 300 positions (256 x 4
+// rows of 2052 positions of 128 bf16: 234 us in 1, 217 in 2, 230 in 3, 239 in 4, 260 in 6).
+// A wave is as many clusters as the device holds at once, which it is asked for: a cluster
+// lies within a group of SMs, and where one CTA fills an SM only 15 clusters of 8 fit the
+// 148 SMs (16 rows: 16.8 us in 8, 11.2 in 6).  Odd numbers leave more SMs of a group idle
+// and are not tried (64 x 4 rows: 66 us in 3, 60 in 1).
+template <auto kern, int GC, int NW, typename Shared>
+cudaError_t launch(const SwaDecodeArgs &a, cudaStream_t stream)
 {
-    const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc;
-    const long long rows = (long long)a.B * a.Hk * nchunk, seen = (long long)a.window + a.sinks, fit = (long long)per_sm * num_sms;
-    int best = 1;
-    double least = 0;
-    for (int n = 1; n <= kMaxSplit; n *= 2) {
-        const double cost = (double)((rows * n + fit - 1) / fit) * ((double)seen / n + 300.0);
-        if (n == 1 || cost < least) least = cost, best = n;
-    }
-    return best;
-}
-
-// GC query heads of a group and NW warps per CTA, PER_SM CTAs on an SM.
-template <auto kern, int GC, int D, int NW, int PER_SM>
-cudaError_t launch(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
-{
-    constexpr int gc = GC, bytes = sizeof(DecodeShared<NW, GC, D>);
     static std::atomic<unsigned long long> set{0};
-    cudaError_t e = ensure_smem_limit(kern, bytes, set);
+    static std::atomic<int> fit[kMaxSplit];  // clusters of n + 1 that fit (the kernels are sm_100a's: the same on every device)
+    cudaError_t e = ensure_smem_limit(kern, sizeof(Shared), set);
     if (e != cudaSuccess) return e;
-    const int G = a.Hq / a.Hk, nchunk = (G + gc - 1) / gc, nsplit = splits(a, gc, PER_SM, num_sms);
+    const int G = a.Hq / a.Hk, nchunk = (G + GC - 1) / GC;
+    const long long rows = (long long)a.B * a.Hk * nchunk, seen = (long long)a.window + a.sinks;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);  // (y is at most the number of query heads)
     cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = nsplit;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int nsplit = 1;
+    double least = 0;
+    for (int n = 1; n <= kMaxSplit; n += n == 1 ? 1 : 2) {
+        int m = fit[n - 1].load(std::memory_order_relaxed);
+        if (m == 0) {
+            attr[0].val.clusterDim.x = n;
+            cfg.gridDim = dim3(n);
+            if ((e = cudaOccupancyMaxActiveClusters(&m, kern, &cfg)) != cudaSuccess) return e;
+            if (m < 1) m = 1;
+            fit[n - 1].store(m, std::memory_order_relaxed);
+        }
+        const double cost = (double)((rows + m - 1) / m) * ((double)seen / n + 300.0);
+        if (n == 1 || cost < least) least = cost, nsplit = n;
+    }
+    attr[0].val.clusterDim.x = nsplit;
+    cfg.gridDim = dim3(nsplit, a.Hk * nchunk, a.B);  // (y is at most the number of query heads)
     cfg.numAttrs = nsplit > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, a, nsplit, nchunk);
 }
 
+template <int D, int HR, int NW, int AHEAD, int PER_SM>
+cudaError_t launch_mma(const SwaDecodeArgs &a, cudaStream_t stream)
+{
+    return launch<decode_mma_kernel<D, HR, NW, AHEAD, PER_SM>, 8 * HR, NW, MmaShared<NW, 8 * HR, D, AHEAD>>(a, stream);
+}
+
 template <int D>
-cudaError_t by_group_f32(const SwaDecodeArgs &a, int num_sms, cudaStream_t stream)
+cudaError_t by_group_f32(const SwaDecodeArgs &a, cudaStream_t stream)
 {
     const int G = a.Hq / a.Hk;
-    if (G == 1) return launch<decode_kernel<float, D, 1>, 1, D, 4, 4>(a, num_sms, stream);
-    if (G == 2) return launch<decode_kernel<float, D, 2>, 2, D, 4, 4>(a, num_sms, stream);
-    return launch<decode_kernel<float, D, 4>, 4, D, 4, 4>(a, num_sms, stream);
+    if (G == 1) return launch<decode_kernel<float, D, 1>, 1, 4, DecodeShared<4, 1, D>>(a, stream);
+    if (G == 2) return launch<decode_kernel<float, D, 2>, 2, 4, DecodeShared<4, 2, D>>(a, stream);
+    return launch<decode_kernel<float, D, 4>, 4, 4, DecodeShared<4, 4, D>>(a, stream);
 }
 
 }  // namespace
@@ -494,16 +552,17 @@ cudaError_t launch_swa_decode(const SwaDecodeArgs &a, bool bf16, int num_sms, cu
 {
     if (bf16) {
         // few rows: eight warps a CTA, so that a warp's walk is short (one sequence, 16 heads of
-        // 128, 2052 slots: 13.8 us with four)
+        // 128, 2052 slots: 11.0 us, and 13.8 with four).  Else as many CTAs on an SM as the
+        // registers allow without spilling (four of 128 threads at d = 128 spill: 292 us
+        // against 216 with three).
         const bool small_group = a.Hq / a.Hk <= 8;
         if (small_group && (long long)a.B * a.Hk * kMaxSplit <= num_sms)
-            return a.d == 128 ? launch<decode_mma_kernel<128, 1, 8>, 8, 128, 8, 1>(a, num_sms, stream)
-                              : launch<decode_mma_kernel<64, 1, 8>, 8, 64, 8, 1>(a, num_sms, stream);
-        if (small_group && a.d == 64) return launch<decode_mma_kernel<64, 1, 4>, 8, 64, 4, 4>(a, num_sms, stream);
-        return a.d == 128 ? launch<decode_mma_kernel<128, 2, 4>, 16, 128, 4, 2>(a, num_sms, stream)
-                          : launch<decode_mma_kernel<64, 2, 4>, 16, 64, 4, 2>(a, num_sms, stream);
+            return a.d == 128 ? launch_mma<128, 1, 8, 2, 1>(a, stream) : launch_mma<64, 1, 8, 2, 1>(a, stream);
+        if (small_group)
+            return a.d == 128 ? launch_mma<128, 1, 4, 1, 3>(a, stream) : launch_mma<64, 1, 4, 2, 4>(a, stream);
+        return a.d == 128 ? launch_mma<128, 2, 4, 2, 2>(a, stream) : launch_mma<64, 2, 4, 2, 4>(a, stream);
     }
-    return a.d == 128 ? by_group_f32<128>(a, num_sms, stream) : by_group_f32<64>(a, num_sms, stream);
+    return a.d == 128 ? by_group_f32<128>(a, stream) : by_group_f32<64>(a, stream);
 }
 
 }  // namespace gdn2
