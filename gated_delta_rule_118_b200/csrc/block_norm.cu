@@ -8,7 +8,10 @@
 // column sums stay in registers.  Rows are fetched ahead into a ring in shared memory by
 // bulk copies (rows whose length is not a multiple of 8 by plain loads): the row sums of
 // one row (two in the forward, three in the backward) would otherwise leave the memory
-// idle.  Bound by HBM.
+// idle.  Bound by HBM: 32768 x 2048 bf16 with a gate, forward 114 us (5.9 TB/s), backward
+// 213 us (5.1; three CTAs an SM, with the column sums in shared memory to fit their
+// registers, leave room for fewer rows fetched ahead: 226 us).  Long rows are bound by the
+// exchange of their sums: 8192 x 8192 forward 150 us (4.5 TB/s), backward 348 (3.1).
 //
 // The backward's sums over rows (for the three vectors' gradients) are added in a fixed
 // order: each CTA over its rows, then a small kernel over the CTAs.  dw_post and
@@ -134,16 +137,24 @@ __device__ __forceinline__ f2 sigmoid2(f2 x)
 template <int NW>
 struct SumSlots {
     alignas(16) float warp[2][2][NW];  // [slot][value][warp]
-    float cta[2][2][4];                // [slot][value][CTA of the cluster]
+    ulonglong2 cta[2][4];              // [slot][CTA of the cluster]: its values
+    uint64_t landed[2];                // [slot]: every CTA's values are here
 };
 template <int NW, bool CL>
 struct RowSums {
     SumSlots<NW> &sl;
+    unsigned int *err;
     int slot = 0;
-    __device__ __forceinline__ explicit RowSums(SumSlots<NW> &slots) : sl(slots)
+    uint32_t ph = 0;
+    __device__ __forceinline__ RowSums(SumSlots<NW> &slots, unsigned int *err_) : sl(slots), err(err_)
     {
         for (int i = threadIdx.x; i < 4 * NW; i += blockDim.x) (&sl.warp[0][0][0])[i] = 0.f;
+        if (CL && threadIdx.x < 2) {
+            sm100::mbar_init(sl.landed + threadIdx.x, 1);
+            sm100::fence_mbar_init();
+        }
         __syncthreads();
+        if constexpr (CL) cg::this_cluster().sync();  // every CTA has started, its barriers set up
     }
     template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N])
@@ -170,17 +181,25 @@ struct RowSums {
             }
         }
         if constexpr (CL) {
+            // each CTA sends its values to all: 16 bytes that signal the receiver's barrier (8192
+            // x 8192 bf16 forward: 150 us, and 229 with a barrier of the whole cluster).  A CTA
+            // that sends for the sum after next has this CTA's values of the next, sent when all
+            // of its threads had read these.
             cg::cluster_group cluster = cg::this_cluster();
             const int size = cluster.num_blocks(), rank = cluster.block_rank();
-            if (threadIdx.x < size)
-#pragma unroll
-                for (int n = 0; n < N; ++n) *cluster.map_shared_rank(&sl.cta[slot][n][rank], threadIdx.x) = v[n];
-            cluster.sync();
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                v[n] = 0.f;
-                for (int c = 0; c < size; ++c) v[n] += sl.cta[slot][n][c];
+            if (threadIdx.x == 0) sm100::mbar_arrive_expect_tx(sl.landed + slot, size * 16);
+            if (threadIdx.x < size) {
+                const ulonglong2 mine = make_ulonglong2(pack2(v[0], N > 1 ? v[N - 1] : 0.f), 0);
+                sm100::st_async_16(sm100::peer_smem(&sl.cta[slot][rank], threadIdx.x), mine,
+                                   sm100::peer_smem(sl.landed + slot, threadIdx.x));
             }
+            sm100::mbar_wait(sl.landed + slot, ph, err);
+            f2 t = 0;
+            for (int c = 0; c < size; ++c) t = add2(t, sl.cta[slot][c].x);
+            const float2 u = unpack2(t);
+            v[0] = u.x;
+            if constexpr (N > 1) v[1] = u.y;
+            if (slot) ph ^= 1;
         }
         slot ^= 1;
     }
@@ -223,7 +242,7 @@ template <typename E, bool VEC, bool CL, int NW>
 __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const NormArgs a, int cols_per_cta, int csize, int stages)
 {
     __shared__ SumSlots<NW> slots;
-    RowSums<NW, CL> sums(slots);
+    RowSums<NW, CL> sums(slots, a.err);
     const int tid = threadIdx.x, nt = blockDim.x;
     const int c0 = CL ? (int)(blockIdx.x % csize) * cols_per_cta : 0, cols = min(a.D, c0 + cols_per_cta);
     const long long first = blockIdx.x / csize, step = gridDim.x / csize;
@@ -290,14 +309,14 @@ __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const N
         for (int i = 0; i < 4; ++i) r1[i] = mul2(r1[i], mul2(ir, wq[i]));
         store_eight<E, VEC>(static_cast<E *>(a.x_out) + n * a.D, r1, c0, tid, nt, cols);
     }
-    if constexpr (CL) cg::this_cluster().sync();  // no CTA leaves while another may still write its slots
+    // (no CTA leaves before all values sent to it have landed: it waits for each of its sums)
 }
 
 template <typename E, bool VEC, bool CL, int NW>
 __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const NormArgs a, int cols_per_cta, int csize, int stages)
 {
     __shared__ SumSlots<NW> slots;
-    RowSums<NW, CL> sums(slots);
+    RowSums<NW, CL> sums(slots, a.err);
     const int tid = threadIdx.x, nt = blockDim.x;
     const int c0 = CL ? (int)(blockIdx.x % csize) * cols_per_cta : 0, cols = min(a.D, c0 + cols_per_cta);
     const long long first = blockIdx.x / csize, step = gridDim.x / csize;
@@ -403,7 +422,6 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             part[a.D + c] = i & 1 ? ps.y : ps.x;
         }
     }
-    if constexpr (CL) cg::this_cluster().sync();
 }
 
 // 32 columns a CTA, its 32 warps over the partial rows: many loads in flight, since each

