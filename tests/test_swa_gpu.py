@@ -180,6 +180,28 @@ def test_repeated_calls_give_identical_bits(dtype):
         assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,Tk,W,S", [(200, 200, 6, 3), (130, 140, 1, 4), (150, 150, 12, 0), (24, 24, 100, 0), (3, 20, 100, 2)])
+def test_few_visible_keys_in_bf16(T, Tk, W, S, d):
+    """Rows that see up to a dozen keys: score gradients carry no rounding of o, and the gradients
+    little but their own (a relative rounding of at most 2^-8, evenly spread: 2^-8 / sqrt(3) in the
+    mean square; operands of 16 bits and fp32 sums stay below 2^-12)."""
+    q, k, v, dO = make(3, T, Tk, 6, 2, d, BF, seed=T + W)
+    lens = torch.tensor([T, T // 2, 0], dtype=torch.int32, device="cuda")
+    got = check(q, k, v, dO, lens, W, S)
+    ref, tol = hybrid.swa(q, k, v, lens, dO, window=W, sinks=S, scale=d ** -0.5)
+    if W + S <= 12 or Tk <= 24:
+        for n in ("dq", "dk"):
+            assert (got[n].double() - ref[n]).norm() <= (2.0 ** -8 / 3 ** 0.5 + 2.0 ** -12) * ref[n].norm(), n
+    for t in (q, dO):
+        t[1, T // 2:] = float("nan")
+    o, lse = g.gdn2_swa_fwd(q, k, v, lens, window=W, sinks=S)
+    # (within the bounds, not bit by bit: a row whose tile holds a NaN is formed again in fp32)
+    again = g.gdn2_swa_bwd(q, k, v, o, lse, dO, lens, window=W, sinks=S)
+    for n in again:
+        close(again[n], ref[n], tol[n], n)
+
+
 def test_gradient_against_differences():
     """Directional derivatives of sum(o * dO), fp32, against central differences of the fp64 forward."""
     q, k, v, dO = make(1, 90, 90, 4, 2, 64, F32, seed=12)
