@@ -379,9 +379,11 @@ int kv_split(const SwaArgs &a, int num_sms)
     return n;
 }
 
-// delta = dO . o of every row that holds a token (0 in the others): 16 bytes a lane, so 8
-// to 32 lanes a row, and kDeltaRows rows a lane.  Bound by HBM.
-constexpr int kDeltaRows = 4;
+// delta = dO . o of every row that holds a token (0 in the others), a sequence in grid y: 16
+// bytes a lane, so 8 to 32 lanes a row, and kDeltaRows rows a lane.  Bound by HBM and the
+// division behind a row's place (4 x 4096 x 16 heads of 128 bf16: 28 us; with four rows a
+// lane and two divisions a row 45).
+constexpr int kDeltaRows = 2;
 __device__ __forceinline__ long long quotient(long long n, int d)  // (64-bit division takes as long as the loads)
 {
     return n < 0x7fffffffLL ? (unsigned)n / (unsigned)d : n / d;
@@ -390,22 +392,22 @@ template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) delta_kernel(const SwaArgs a)
 {
     constexpr int W = 16 / sizeof(E), LPR = D / W, RPC = kThreads / LPR;  // elements a lane, lanes a row, rows at a time
-    const long long rows = (long long)a.B * a.T * a.Hq, row0 = (long long)blockIdx.x * (RPC * kDeltaRows) + threadIdx.x / LPR;
-    const int x = threadIdx.x % LPR * W;
+    const long long rows = (long long)a.T * a.Hq, row0 = (long long)blockIdx.x * (RPC * kDeltaRows) + threadIdx.x / LPR;
+    const int x = threadIdx.x % LPR * W, b = blockIdx.y, n = seq_len(a, b);
+    const E *o_seq = static_cast<const E *>(a.o) + b * rows * D, *g_seq = static_cast<const E *>(a.dO) + b * rows * D;
     uint4 o[kDeltaRows], g[kDeltaRows];
     bool live[kDeltaRows];
     long long to[kDeltaRows];
 #pragma unroll
     for (int u = 0; u < kDeltaRows; ++u) {
-        const long long row = row0 + u * RPC;  // (b, t, h)
-        const long long bt = quotient(row, a.Hq);
-        const int h = (int)(row - bt * a.Hq), b = (int)quotient(bt, a.T), t = (int)(bt - (long long)b * a.T);
-        live[u] = row < rows && t < seq_len(a, b);
+        const long long row = row0 + u * RPC;  // (t, h)
+        const int t = (int)quotient(row, a.Hq), h = (int)(row - (long long)t * a.Hq);
+        live[u] = row < rows && t < n;
         to[u] = row < rows ? ((long long)b * a.Hq + h) * a.T + t : -1;
         o[u] = g[u] = make_uint4(0, 0, 0, 0);
         if (live[u]) {
-            o[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.o) + row * D + x);
-            g[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.dO) + row * D + x);
+            o[u] = *reinterpret_cast<const uint4 *>(o_seq + row * D + x);
+            g[u] = *reinterpret_cast<const uint4 *>(g_seq + row * D + x);
         }
     }
 #pragma unroll
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) delta_kernel(const SwaArgs a)
 // few keys: there dO . o carries the roundings of o and of the forward's P undiminished into
 // every dS of the row (relative error of dq 2.9e-3 with 4 visible keys, 2.5e-3 with 8, 2.2e-3
 // with 16, the outputs' own rounding being 1.7e-3), and a row's scores are quickly formed
-// again (4 x 4096 x 16 heads of 128, window 12: 511 us of backward, and 342 without).
+// again (4 x 4096 x 16 heads of 128, window 12: 509 us of backward, and 320 without).
 // Short sequences see half of their keys on average.
 constexpr int kFewKeys = 12;
 template <int D>
@@ -432,10 +434,9 @@ __global__ void __launch_bounds__(kThreads) delta_few_kernel(const SwaArgs a)
 {
     using E = __nv_bfloat16;
     constexpr int LPR = D / 8;
-    const long long row = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;  // (b, t, h)
-    const bool in = row < (long long)a.B * a.T * a.Hq;
-    const long long bt = quotient(in ? row : 0, a.Hq);
-    const int h = (int)((in ? row : 0) - bt * a.Hq), b = (int)quotient(bt, a.T), t = (int)(bt - (long long)b * a.T);
+    const long long row = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;  // (t, h)
+    const bool in = row < (long long)a.T * a.Hq;
+    const int b = blockIdx.y, t = in ? (int)quotient(row, a.Hq) : 0, h = in ? (int)(row - (long long)t * a.Hq) : 0;
     const bool live = in && t < seq_len(a, b);
     const int x = threadIdx.x % LPR * 8, hk = h / (a.Hq / a.Hk);
     const long long out = ((long long)b * a.Hq + h) * a.T + t;
@@ -520,9 +521,9 @@ cudaError_t delta_impl(const SwaArgs &a, cudaStream_t stream)
 {
     const bool few = sizeof(E) == 2 && ((long long)a.window + a.sinks <= kFewKeys || a.Tk <= 2 * kFewKeys);
     const int per = kThreads * 16 / (D * (int)sizeof(E)) * (few ? 1 : kDeltaRows);
-    const long long rows = (long long)a.B * a.T * a.Hq, blocks = (rows + per - 1) / per;
+    const long long rows = (long long)a.T * a.Hq, blocks = (rows + per - 1) / per;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_plain(few ? delta_few_kernel<D> : delta_kernel<E, D>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+    return launch_plain(few ? delta_few_kernel<D> : delta_kernel<E, D>, dim3((unsigned)blocks, a.B), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
