@@ -132,8 +132,11 @@ import gated_delta_rule_118_b200 as g
 x = torch.randn(2, 300, 128, device="cuda")
 v = torch.ones(128, device="cuda")
 q = torch.randn(1, 300, 2, 128, device="cuda").bfloat16()
+t, cache = q[0, :4], q[0, :280].view(4, 70, 2, 128).clone()
+pos = torch.tensor([5, 69, 70, -1], dtype=torch.int32, device="cuda")
 calls = dict(swa_fwd=lambda: g.gdn2_swa_fwd(q, q, q, window=64, sinks=2)[0],
              swa_bwd=lambda: g.gdn2_swa_bwd(q, q, q, q, torch.zeros(1, 2, 300, device="cuda"), q, window=64)["dq"],
+             decode=lambda: g.gdn2_swa_decode(t, t, t, cache, cache + 1, pos, window=64, sinks=2),
              scan=lambda: g.gdn2_scan_fwd(x, x, -x.abs())[0],
              norm_bwd=lambda: g.gdn2_block_norm_bwd(x, x, x, v, v, v, x, x)["dr"])
 torch.cuda.synchronize()
@@ -146,7 +149,7 @@ assert torch.equal(out, calls["%s"]())
 """
 
 
-@pytest.mark.parametrize("call", ["swa_fwd", "swa_bwd", "scan", "norm_bwd"])
+@pytest.mark.parametrize("call", ["swa_fwd", "swa_bwd", "decode", "scan", "norm_bwd"])
 def test_the_first_call_of_a_process_can_be_captured(call):
     r = subprocess.run([sys.executable, "-c", FIRST_CALL % (call, call)], cwd=Path(__file__).resolve().parents[1],
                        capture_output=True, text=True, timeout=300)
