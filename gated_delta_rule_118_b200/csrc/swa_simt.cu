@@ -26,6 +26,29 @@ __device__ __forceinline__ void load_rows(float *dst, const Rows<E> &src, int r0
     }
 }
 
+// The same without waiting: copies of one group, ended by rows_asked.
+template <typename E, int D, int N>
+__device__ __forceinline__ void ask_rows(float *dst, const Rows<E> &src, int r0, int end)
+{
+    static_assert(sizeof(E) == 4, "rows are copied as they are");
+#pragma unroll
+    for (int c = threadIdx.x; c < N * D / 4; c += kThreads) {
+        const int r = c / (D / 4), x = c % (D / 4) * 4;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * (D + 4) + x);
+        const int bytes = r0 + r < end ? 16 : 0;  // (the rest of the 16 is filled with zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src[min(r0 + r, end - 1)] + x), "r"(bytes) : "memory");
+    }
+}
+__device__ __forceinline__ void rows_asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>
+__device__ __forceinline__ void rows_landed()  // all groups but the last LATER
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+}
+// Tiles are asked for one ahead at d = 64.  At d = 128 the second buffer would cost the
+// second CTA of an SM.
+constexpr int tiles_ahead(int d) { return d == 64 ? 1 : 0; }
+
 // s[i][j] += A[ra + i] . B[cb + 16 j] over D.
 template <int D, int NI, int NJ>
 __device__ __forceinline__ void dot_tile(float (&s)[NI][NJ], const float *A, int ra, const float *B, int cb)
@@ -123,9 +146,9 @@ __device__ __forceinline__ bool store_cols(E *dst, const float (&acc)[D / 16], f
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
 {
-    constexpr int LD = D + 4, PS = 68;
+    constexpr int LD = D + 4, PS = 68, AHEAD = tiles_ahead(D);
     extern __shared__ float sm[];
-    float *Qs = sm, *KV = Qs + 64 * LD, *Ps = KV + 64 * LD;
+    float *Qs = sm, *Ks = Qs + 64 * LD, *Vs = Ks + AHEAD * 64 * LD, *Ps = Vs + 64 * LD;  // (one after the other in one place, or each its own)
     __shared__ unsigned bad[2];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int i0 = (gridDim.x - 1 - blockIdx.x) * 64, h = blockIdx.y, b = blockIdx.z;  // longest rows first
@@ -141,13 +164,18 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
         load_rows<E, D, 64>(Qs, q, i0, n);
         const int p0 = off + i0, p1 = off + min(i0 + 64, n) - 1;
         const KeyTiles kt(p0, p1, a.window, a.sinks, 64);
+        if (AHEAD) ask_rows<E, D, 64>(Ks, k, kt.tile(0) * 64, a.Tk);
+        rows_asked();
         for (int c = 0; c < kt.count(); ++c) {
             const int j0 = kt.tile(c) * 64;
             __syncthreads();
-            load_rows<E, D, 64>(KV, k, j0, a.Tk);
+            if (AHEAD) ask_rows<E, D, 64>(Vs, v, j0, a.Tk);
+            else ask_rows<E, D, 64>(Ks, k, j0, a.Tk);
+            rows_asked();
+            rows_landed<AHEAD>();
             __syncthreads();
             float s[4][4] = {};
-            dot_tile<D, 4, 4>(s, Qs, ty * 4, KV, tx);
+            dot_tile<D, 4, 4>(s, Qs, ty * 4, Ks, tx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float mx = -INFINITY;
@@ -172,9 +200,12 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
                 for (int u = 0; u < D / 16; ++u) o[i][u] *= f;
             }
             __syncthreads();
-            load_rows<E, D, 64>(KV, v, j0, a.Tk);
+            if (!AHEAD) ask_rows<E, D, 64>(Vs, v, j0, a.Tk);
+            else if (c + 1 < kt.count()) ask_rows<E, D, 64>(Ks, k, kt.tile(c + 1) * 64, a.Tk);
+            rows_asked();
+            rows_landed<AHEAD>();
             __syncthreads();
-            mul_tile<D, 64, PS>(o, Ps, ty * 4, KV, tx);
+            mul_tile<D, 64, PS>(o, Ps, ty * 4, Vs, tx);
         }
     }
     __syncthreads();
@@ -200,9 +231,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
 {
-    constexpr int LD = D + 4, PS = 36;
+    constexpr int LD = D + 4, PS = 36, AHEAD = tiles_ahead(D);
     extern __shared__ float sm[];
-    float *Qs = sm, *Gs = Qs + 64 * LD, *Ks = Gs + 64 * LD, *Vs = Ks + 32 * LD, *Ps = Vs + 32 * LD;
+    float *Qs = sm, *Gs = Qs + 64 * LD, *tiles = Gs + 64 * LD, *Ps = tiles + (1 + AHEAD) * 64 * LD;  // tiles: K, V
     __shared__ unsigned bad[2];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int i0 = (gridDim.x - 1 - blockIdx.x) * 64, h = blockIdx.y, b = blockIdx.z;
@@ -224,11 +255,21 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
         }
         const int p0 = off + i0, p1 = off + min(i0 + 64, n) - 1;
         const KeyTiles kt(p0, p1, a.window, a.sinks, 32);
+        auto ask = [&](int c) {
+            if (c < kt.count()) {
+                float *to = tiles + (AHEAD ? c & 1 : 0) * 64 * LD;
+                ask_rows<E, D, 32>(to, k, kt.tile(c) * 32, a.Tk);
+                ask_rows<E, D, 32>(to + 32 * LD, v, kt.tile(c) * 32, a.Tk);
+            }
+            rows_asked();
+        };
+        if (AHEAD) ask(0);
         for (int c = 0; c < kt.count(); ++c) {
             const int j0 = kt.tile(c) * 32;
+            const float *Ks = tiles + (AHEAD ? c & 1 : 0) * 64 * LD, *Vs = Ks + 32 * LD;
             __syncthreads();
-            load_rows<E, D, 32>(Ks, k, j0, a.Tk);
-            load_rows<E, D, 32>(Vs, v, j0, a.Tk);
+            ask(c + AHEAD);
+            rows_landed<AHEAD>();
             __syncthreads();
             float s[4][2] = {}, dp[4][2] = {};
             dot_tile<D, 4, 2>(s, Qs, ty * 4, Ks, tx);
@@ -266,9 +307,9 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a, int nsplit, float *part)
 {
-    constexpr int LD = D + 4, PS = 68;
+    constexpr int LD = D + 4, PS = 68, AHEAD = tiles_ahead(D);
     extern __shared__ float sm[];
-    float *Ks = sm, *Vs = Ks + 64 * LD, *Qs = Vs + 64 * LD, *Gs = Qs + 32 * LD, *Ps = Gs + 32 * LD;
+    float *Ks = sm, *Vs = Ks + 64 * LD, *tiles = Vs + 64 * LD, *Ps = tiles + (1 + AHEAD) * 64 * LD;  // tiles: Q, dO
     __shared__ unsigned bad[2];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int j0 = (int)(blockIdx.x / nsplit) * 64, split = blockIdx.x % nsplit, hk = blockIdx.y, b = blockIdx.z;
@@ -282,14 +323,25 @@ __global__ void __launch_bounds__(kThreads) dkdv_kernel(const SwaArgs a, int nsp
     const int i_hi = (j0 < a.sinks || far > n) ? n : (int)far;
     const int nq = i_hi > i_lo ? (i_hi - i_lo + 31) / 32 : 0;
     const long long all = (long long)G * nq, per = (all + nsplit - 1) / nsplit;
-    for (long long it = split * per; it < min(all, (split + 1) * per); ++it) {
+    const long long it0 = split * per, it1 = min(all, (split + 1) * per);
+    auto ask = [&](long long it) {
+        if (it < it1) {
+            const int h = hk * G + (int)(it / nq), i0 = i_lo + (int)(it % nq) * 32;
+            float *to = tiles + (AHEAD ? (it - it0) & 1 : 0) * 64 * LD;
+            ask_rows<E, D, 32>(to, rows_of<E>(a.q, a.qs, b, h), i0, n);
+            ask_rows<E, D, 32>(to + 32 * LD, dense_rows<E>(a.dO, b, h, a.T, a.Hq, D), i0, n);
+        }
+        rows_asked();
+    };
+    if (AHEAD) ask(it0);
+    for (long long it = it0; it < it1; ++it) {
         const int h = hk * G + (int)(it / nq), i0 = i_lo + (int)(it % nq) * 32;
-        const Rows<E> q = rows_of<E>(a.q, a.qs, b, h), g = dense_rows<E>(a.dO, b, h, a.T, a.Hq, D);
         const long long lrow = ((long long)b * a.Hq + h) * a.T;
+        const float *Qs = tiles + (AHEAD ? (it - it0) & 1 : 0) * 64 * LD, *Gs = Qs + 32 * LD;
         {
             __syncthreads();
-            load_rows<E, D, 32>(Qs, q, i0, n);
-            load_rows<E, D, 32>(Gs, g, i0, n);
+            ask(it + AHEAD);
+            rows_landed<AHEAD>();
             __syncthreads();
             float s[2][4] = {}, dp[2][4] = {};
             dot_tile<D, 2, 4>(s, Qs, ty * 2, Ks, tx);
@@ -490,7 +542,7 @@ __global__ void __launch_bounds__(kThreads) delta_few_kernel(const SwaArgs a)
 template <typename E, int D>
 cudaError_t fwd_impl(const SwaArgs &a, cudaStream_t stream)
 {
-    constexpr int bytes = sizeof(float) * (2 * 64 * (D + 4) + 64 * 68);
+    constexpr int bytes = sizeof(float) * ((2 + tiles_ahead(D)) * 64 * (D + 4) + 64 * 68);
     static std::atomic<unsigned long long> set{0};
     const cudaError_t e = ensure_smem_limit(fwd_kernel<E, D>, bytes, set);
     if (e != cudaSuccess) return e;
@@ -500,7 +552,7 @@ cudaError_t fwd_impl(const SwaArgs &a, cudaStream_t stream)
 template <typename E, int D>
 cudaError_t bwd_impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
 {
-    constexpr int dq_bytes = sizeof(float) * (192 * (D + 4) + 64 * 36), kv_bytes = sizeof(float) * (192 * (D + 4) + 32 * 68);
+    constexpr int rows = 192 + tiles_ahead(D) * 64, dq_bytes = sizeof(float) * (rows * (D + 4) + 64 * 36), kv_bytes = sizeof(float) * (rows * (D + 4) + 32 * 68);
     static std::atomic<unsigned long long> dq_set{0}, kv_set{0};
     cudaError_t e = ensure_smem_limit(dq_kernel<E, D>, dq_bytes, dq_set);
     if (e == cudaSuccess) e = ensure_smem_limit(dkdv_kernel<E, D>, kv_bytes, kv_set);
