@@ -3,8 +3,9 @@
 // tiles).  The products are 64-wide register tiles over shared memory; bound by
 // the FFMA rate (every score costs 2 d FMAs, and the two-kernel backward forms
 // q k^T and dO v^T twice in exchange for a fixed order of every sum).  3 x 333 x 6 heads
-// of 64 over 2, window 100, forward and backward: 131 us in five launches, each a fraction
-// of a wave, so bound by the walk of one CTA.
+// of 64 over 2, window 100, forward and backward: 125 us in five launches, each a fraction
+// of a wave, so bound by the walk of one CTA; 2 x 4096 x 8 heads of 64, window 512: forward
+// 342 us, backward 2016, a quarter of the FFMA rate, for the barriers between a tile's steps.
 #include "launch.h"
 #include "swa_common.cuh"
 
