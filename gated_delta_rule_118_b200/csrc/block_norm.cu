@@ -11,7 +11,7 @@
 // idle.  Bound by HBM: 32768 x 2048 bf16 with a gate, forward 114 us (5.9 TB/s), backward
 // 213 us (5.1; three CTAs an SM, with the column sums in shared memory to fit their
 // registers, leave room for fewer rows fetched ahead: 226 us).  Long rows are bound by the
-// exchange of their sums: 8192 x 8192 forward 150 us (4.5 TB/s), backward 348 (3.1).
+// exchange of their sums: 8192 x 8192 forward 149 us (4.5 TB/s), backward 352 (3.1).
 //
 // The backward's sums over rows (for the three vectors' gradients) are added in a fixed
 // order: each CTA over its rows, then a small kernel over the CTAs.  dw_post and
@@ -118,17 +118,34 @@ __device__ __forceinline__ int column(int c0, int tid, int nt, int i)
     return VEC ? c0 + tid * 8 + i : c0 + tid + i * nt;
 }
 
-// 1 / (1 + 2^(-x log2 e)): both steps are accurate to about 2^-22, which the sums over
-// rows need (a half-precision hyperbolic tangent would show in their gradients).
-__device__ __forceinline__ f2 sigmoid2(f2 x)
+// 1 / (1 + e), e = 2^(-x log2 e): both steps are accurate to about 2^-22, which the sums over
+// rows need (a half-precision hyperbolic tangent would show in their gradients).  Also gives e,
+// and raises `far` to the largest exponent's magnitude.
+__device__ __forceinline__ f2 sigmoid2(f2 x, f2 &e, float &far)
 {
     float2 t = unpack2(mul2(x, both(-1.4426950408889634f)));
+    far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.y));
-    t = unpack2(add2(pack2(t.x, t.y), both(1.f)));
+    e = pack2(t.x, t.y);
+    t = unpack2(add2(e, both(1.f)));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.x));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.y));
     return pack2(t.x, t.y);
+}
+__device__ __forceinline__ f2 sigmoid2(f2 x)
+{
+    f2 e;
+    float far = 0.f;
+    return sigmoid2(x, e, far);
+}
+// e as a factor of 1 - sigmoid = e * sigmoid, where an exponent beyond 54 occurs: 0 where the
+// sigmoid is 1 in double precision too, and short of infinity, which the 0 of a closed gate
+// must not meet.  (A NaN stays in the sigmoid.)
+__device__ __forceinline__ f2 bounded(f2 e)
+{
+    const float2 t = unpack2(e);
+    return pack2(t.x < 0x1p-54f ? 0.f : fminf(t.x, 0x1p125f), t.y < 0x1p-54f ? 0.f : fminf(t.y, 0x1p125f));
 }
 
 // Sums of N values over the CTA (NW warps at most; absent ones leave zeros), and over
@@ -355,15 +372,20 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             dx.from_memory(static_cast<const E *>(a.dx_out) + n * a.D, c0, tid, nt, cols);
             dr.from_memory(static_cast<const E *>(a.dr_out) + n * a.D, c0, tid, nt, cols);
         }
-        f2 yv[4], r1[4], gt[4], xv[4], dv[4], sq = 0, sx = 0;
+        f2 yv[4], r1[4], gt[4], ge[4], xv[4], dv[4], sq = 0, sx = 0;
+        float far = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             yv[i] = y[i];
             r1[i] = r[i];
-            gt[i] = a.g ? sigmoid2(g[i]) : both(1.f);
+            gt[i] = a.g ? sigmoid2(g[i], ge[i], far) : both(1.f);
             xv[i] = dx[i];
             dv[i] = dr[i];
             sq = fma2(yv[i], yv[i], sq);
+        }
+        if (__builtin_expect(far > 54.f, 0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ge[i] = bounded(ge[i]);
         }
         float s[1] = {sum2(sq)};
         sums(s);
@@ -407,7 +429,9 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             const f2 b = mul2(xv[i], yv[i]), bt = mul2(b, t[i]);
             bsum[i] = add2(bsum[i], b);
             r1[i] = mul2(iy, fma2(my, yv[i], r1[i]));
-            dv[i] = fma2(bt, mul2(gt[i], both(-1.f)), bt);
+            // 1 - gate as e * gate: the difference has 3 % of itself left at a logit of 12, and
+            // nothing above 17
+            if (a.g) dv[i] = mul2(bt, mul2(ge[i], gt[i]));
         }
         store_eight<E, VEC>(static_cast<E *>(a.dy) + n * a.D, r1, c0, tid, nt, cols);
         if (a.g) store_eight<E, VEC>(static_cast<E *>(a.dg) + n * a.D, dv, c0, tid, nt, cols);

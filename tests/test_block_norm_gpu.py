@@ -134,3 +134,26 @@ def test_more_than_2_31_elements():
     ref, tol = hybrid.block_norm(r[-5:], y[-5:], None, *vec, EPS)
     close(r_out[-5:], ref["r_out"], tol["r_out"], "r_out")
     close(x_out[-5:], ref["x_out"], tol["x_out"], "x_out")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 1001, 4096, 8200])
+def test_logit_gradients_of_gates_between_closed_and_open(D, dtype):
+    """dg_logit is proportional to gate * (1 - gate): both keep their relative accuracy, so the
+    gradient of a gate at 1 - 1e-7 is right and not the rounding of the gate."""
+    args, dr, dx = make((6, D), dtype, True, seed=8)
+    args[2] = torch.linspace(-20, 20, 6 * D, device="cuda").view(6, D).to(dtype)
+    got = check(args, dr, dx)
+    ref, _ = hybrid.block_norm(*args, EPS, dr, dx, u=U[dtype])
+    open_ = args[2] > 10
+    err = (got["dg_logit"].double() - ref["dg_logit"])[open_].norm() / ref["dg_logit"][open_].norm()
+    # its own rounding (evenly spread, U / sqrt(3)); e^-20 is formed within 20 * 2^-24, sums within a few 2^-24
+    assert err <= U[dtype] / 3 ** 0.5 + 2.0 ** -18, err
+    for far in (-120.0, 120.0, float("-inf"), float("inf")):
+        args[2] = torch.full_like(args[2], far)
+        got = g.gdn2_block_norm_bwd(*args, dr, dx, EPS)
+        assert (got["dg_logit"] == 0).all() and all(got[n].isfinite().all() for n in got)
+    args[2] = torch.zeros_like(args[2])
+    args[2][2, 3] = float("nan")
+    got = g.gdn2_block_norm_bwd(*args, dr, dx, EPS)
+    assert got["dg_logit"][2, 3].isnan() and got["dg_logit"][[0, 1, 3, 4, 5]].isfinite().all()
