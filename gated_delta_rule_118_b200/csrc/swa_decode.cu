@@ -263,9 +263,9 @@ __device__ __forceinline__ uint32_t pair_bf16(float x, float y)
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void copy16(uint32_t smem, const void *p)
+__device__ __forceinline__ void copy16(uint32_t smem, const void *p, uint32_t bytes = 16)  // (16, or 0: zeros arrive)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(p), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_group_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) decode_mma_kernel(const SwaDe
 
     const int per = (vis.n + nsplit - 1) / nsplit;
     const int t0 = split * per, t1 = min(vis.n, t0 + per);
-    // rows behind the run read its last position again; their scores are masked
+    // rows behind the run stand at its last position again: their scores are masked, and their
+    // values are zeros (an infinity that the last position holds would meet their weight of 0)
     auto row = [&](const E *fresh, const E *cache, int t) {
         const int p = vis.position(t < t1 ? t : t1 - 1);
         return p == P ? fresh : cache + vis.slot(p) * cstep;
@@ -353,9 +354,11 @@ __global__ void __launch_bounds__(NW * 32, PER_SM) decode_mma_kernel(const SwaDe
         if (t < t1) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const E *p = row(vn, vc, t + 2 * c + (r & 1) + (r >> 1) * 8) + gr * 8;
+                const int tr = t + 2 * c + (r & 1) + (r >> 1) * 8;
+                const E *p = row(vn, vc, tr) + gr * 8;
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) copy16(ring_at + (AHEAD + slot) * Shared::STEP + (r * (D / 64) + j) * 512, p + j * 64);
+                for (int j = 0; j < D / 64; ++j)
+                    copy16(ring_at + (AHEAD + slot) * Shared::STEP + (r * (D / 64) + j) * 512, p + j * 64, tr < t1 ? 16 : 0);
             }
         }
         copy_group_end();

@@ -315,6 +315,29 @@ def test_decode_leaves_rows_without_a_sequence_alone_and_ignores_unseen_slots(dt
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [2, 80])
+def test_decode_of_an_infinite_value_that_is_seen(B, d, dtype):
+    """An infinity in a visible value row reaches its channel as an infinity, also where that row
+    is the last of a run of positions (whose length is seldom a multiple of a step)."""
+    window, sinks = 45, 2
+    slots = window + sinks
+    for P in (0, 6, 17, 40, 46, 100):
+        seen = [p for p in range(P + 1) if p < sinks or P - p < window]
+        for at in {seen[0], seen[len(seen) // 2], seen[-2] if P else 0, seen[-1]}:
+            q, k, v, kc, vc = decode_case(B, slots, 12, 4, d, dtype, seed=P)
+            pos = torch.full((B,), P, dtype=torch.int32, device="cuda")
+            row = v if at == P else vc[:, at if at < sinks else sinks + (at - sinks) % window]
+            row[:, :, 5], row[:, :, 9] = math.inf, -math.inf
+            ref = hybrid.swa_decode(q[:2], k[:2], v[:2], kc[:2], vc[:2], pos[:2], window=window, sinks=sinks, scale=d ** -0.5)[0]
+            o = g.gdn2_swa_decode(q, k, v, kc, vc, pos, window=window, sinks=sinks)
+            assert (o[..., 5] == math.inf).all() and (o[..., 9] == -math.inf).all(), (P, at)
+            rest = [c for c in range(d) if c not in (5, 9)]
+            # roundings of the probabilities and of o, and fp32 sums: as the bounds elsewhere, of values up to 6
+            assert ((o[:2].double() - ref)[..., rest].abs() <= 2 * U[dtype] * 6 + 1e-4).all(), (P, at)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_decode_strided_graph_and_large_cache(dtype):
     """Views of a packed projection, inside a captured graph whose position advances on the device,
     with a cache of more than 2^31 bytes."""
