@@ -41,8 +41,8 @@ using namespace sm100;
 
 constexpr int kThreads = 384;  // two warpgroups that compute, then the issuing warps
 constexpr int kTma = 8, kMma = 9, kRows = 10;
-// 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 = 384 x 168
-constexpr int kRegsCompute = 216, kRegsIssue = 72;
+// 384 threads launch with 168 registers each: 2 x 128 x 208 + 128 x 88 = 384 x 168
+constexpr int kRegsCompute = 208, kRegsIssue = 88;
 
 template <int D>
 struct Tiles {
@@ -189,7 +189,7 @@ struct KvLayout {
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
 };
 
-template <int D>
+template <int D, bool LENS>
 __global__ void __launch_bounds__(kThreads, 1)
 dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __grid_constant__ CUtensorMap mq,
                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -286,6 +286,12 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
+                const int rows = n - w.q * 128;  // behind them is padding
+                if (LENS && n < a.T && rows < 128) {
+                    if (!__all_sync(~0u, mbar_wait(bar + QG_FULL + s, (i >> 1) & 1, a.err))) break;
+                    zero_rows<D>(sm + L::Q + s * L::TILE, rows);
+                    zero_rows<D>(sm + L::G + s * L::TILE, rows);
+                }
                 if (lane == 0) mbar_arrive(bar + EXT_FULL + s);
             }
         } else if (warp == kMma && N > 0) {
@@ -413,7 +419,7 @@ dkdv_tc_kernel(const __grid_constant__ SwaArgs a, const KvPlan plan, const __gri
                 uint32_t *bads = reinterpret_cast<uint32_t *>(sm + L::BADS);
                 bads[hf * 128 + r] = bad;
                 named_bar(1, 256);
-                unsigned todo = __ballot_sync(~0u, hf == 0 && (bads[r] | bads[128 + r]));
+                unsigned todo = __ballot_sync(~0u, bads[r] | bads[128 + r]) & (hf ? 0xffff0000u : 0xffffu);
                 while (todo) {
                     const int r0 = __ffs(todo) - 1;
                     todo &= todo - 1;
@@ -470,7 +476,7 @@ struct QLayout {
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // two buffers of dP
 };
 
-template <int D>
+template <int D, bool LENS>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensorMap mq,
              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -587,6 +593,8 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
+                // zeros for the padding (the scores, which read this tile too, have been taken)
+                if (LENS && c == N - 1 && n < a.T) zero_rows<D>(sm + L::K + ks * L::TILE, min(off + n - kt.tile(c) * 128, 128));
                 if (elect_one()) {
                     issue_cols<D, true>(tmem + L::TM_DQ, tmem + L::TM_DP + s * 128, dk + ks * Tiles<D>::STEP, c > 0);
                     umma_commit(bar + DQ_DONE + s);
@@ -657,7 +665,7 @@ dq_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtensor
             uint32_t *bads = reinterpret_cast<uint32_t *>(sm + L::BAD);
             bads[hf * 128 + r] = bad;
             named_bar(1, 256);
-            unsigned todo = __ballot_sync(~0u, hf == 0 && (bads[r] | bads[128 + r]));
+            unsigned todo = __ballot_sync(~0u, bads[r] | bads[128 + r]) & (hf ? 0xffff0000u : 0xffffu);
             while (todo) {
                 const int r0 = __ffs(todo) - 1;
                 todo &= todo - 1;
@@ -688,14 +696,16 @@ KvPlan plan_kv(const SwaArgs &a, int num_sms)
     return p;
 }
 
-template <int D>
+// LENS: sequences have lengths, so tiles may hold padding.  (Without them the kernels leave the
+// code for it out: 1 x 4096, 16 heads of 128: 252 us, and 257 with it; of 64: 211 and 221.)
+template <int D, bool LENS>
 cudaError_t impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
 {
     KvPlan plan = plan_kv(a, num_sms);
     plan.part = part;
     static std::atomic<unsigned long long> kv_set{0}, q_set{0};
-    cudaError_t e = ensure_smem_limit(dkdv_tc_kernel<D>, KvLayout<D>::BYTES, kv_set);
-    if (e == cudaSuccess) e = ensure_smem_limit(dq_tc_kernel<D>, QLayout<D>::BYTES, q_set);
+    cudaError_t e = ensure_smem_limit(dkdv_tc_kernel<D, LENS>, KvLayout<D>::BYTES, kv_set);
+    if (e == cudaSuccess) e = ensure_smem_limit(dq_tc_kernel<D, LENS>, QLayout<D>::BYTES, q_set);
     if (e != cudaSuccess) return e;
     const long long gs[3] = {(long long)a.T * a.Hq * D, (long long)a.Hq * D, D};
     CUtensorMap mq, mk, mv, mg;
@@ -703,9 +713,9 @@ cudaError_t impl(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream
         !make_rows_map(&mv, a.v, D, a.Hk, a.Tk, a.B, a.vs, 128) || !make_rows_map(&mg, a.dO, D, a.Hq, a.T, a.B, gs, 128))
         return cudaErrorInvalidValue;
     const int items = plan.nseg ? plan.nsink * plan.nseg + plan.ntiles - plan.nsink : plan.ntiles;
-    e = launch_plain(dkdv_tc_kernel<D>, dim3(a.Hk, a.B, items), dim3(kThreads), KvLayout<D>::BYTES, stream, a, plan, mq, mk, mv, mg);
+    e = launch_plain(dkdv_tc_kernel<D, LENS>, dim3(a.Hk, a.B, items), dim3(kThreads), KvLayout<D>::BYTES, stream, a, plan, mq, mk, mv, mg);
     if (e == cudaSuccess)
-        e = launch_plain(dq_tc_kernel<D>, dim3(a.Hq, a.B, (a.T + 127) / 128), dim3(kThreads), QLayout<D>::BYTES, stream, a, mq, mk,
+        e = launch_plain(dq_tc_kernel<D, LENS>, dim3(a.Hq, a.B, (a.T + 127) / 128), dim3(kThreads), QLayout<D>::BYTES, stream, a, mq, mk,
                          mv, mg);
     if (e == cudaSuccess && plan.nseg && plan.nsink)
         e = launch_plain(sink_sum_kernel<D>, dim3(plan.nsink * 16, a.Hk, a.B), dim3(256), 0, stream, a, plan);
@@ -722,7 +732,8 @@ size_t swa_bwd_tc_partial_floats(const SwaArgs &a, int num_sms)
 
 cudaError_t launch_swa_bwd_tc(const SwaArgs &a, float *part, int num_sms, cudaStream_t stream)
 {
-    return a.d == 128 ? impl<128>(a, part, num_sms, stream) : impl<64>(a, part, num_sms, stream);
+    if (a.lens) return a.d == 128 ? impl<128, true>(a, part, num_sms, stream) : impl<64, true>(a, part, num_sms, stream);
+    return a.d == 128 ? impl<128, false>(a, part, num_sms, stream) : impl<64, false>(a, part, num_sms, stream);
 }
 
 }  // namespace gdn2

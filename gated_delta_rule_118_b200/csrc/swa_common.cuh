@@ -8,12 +8,15 @@
 // Masked places and non-finite values: the tile kernels select masked scores away
 // before the exponential, but their second products still multiply a zero
 // probability with whatever stands in a masked row of v (k, q, dO in the
-// backward), and 0 * NaN or 0 * infinity is NaN.  Scrubbing every tile would cost
-// shared-memory bandwidth on every call, so a kernel instead looks at the row it
-// is about to write: if it is not finite, the row is computed again from memory by
+// backward), and 0 * NaN or 0 * infinity is NaN.  Rows of padding are therefore zeros in
+// shared memory (only the tile at a sequence's end has any).  Scrubbing the other tiles
+// would cost shared-memory bandwidth on every call, so a kernel instead looks at the row
+// it is about to write: if it is not finite, the row is computed again from memory by
 // one of the functions below, which touch visible keys only (unless its own row holds a
-// NaN, which reaches all of it).  Finite inputs never
-// take that path; a row that is NaN by its own visible inputs comes out NaN again.
+// NaN, which reaches all of it).  That takes one warp a row and is slow; it is for tokens
+// of a sequence that are not finite, and for bf16 values beyond 2^67 or so, which a
+// probability of up to 2^60 (relative to the row's reference) can take to infinity.  A
+// row that is NaN by its own visible inputs comes out NaN again.
 #pragma once
 
 #include "common.cuh"
@@ -52,6 +55,20 @@ struct KeyTiles {
     __device__ __forceinline__ int count() const { return nsink + w1 - w0; }
     __device__ __forceinline__ int tile(int n) const { return n < nsink ? n : w0 + n - nsink; }
 };
+
+// Rows [first, 128) of a tile in shared memory (boxes of 128 rows x 64 bf16 with the 128-byte
+// swizzle, which stays within a row) set to zero by one warp, for tensor-core reads that
+// follow a barrier.  What stands in the padding behind a sequence is not to meet a zero
+// probability: not being finite, it would make every row of its tile be formed again.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int first)
+{
+    for (int x = 0; x < D / 64; ++x)
+        for (int c = first * 8 + (threadIdx.x & 31); c < 128 * 8; c += 32)
+            *reinterpret_cast<uint4 *>(tile + x * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
 
 // Whether all of keys [j0, j1) are visible to all of positions [p0, p1].
 __device__ __forceinline__ bool tile_full(int p0, int p1, int j0, int j1, int window, int sinks)

@@ -66,7 +66,9 @@ enum { Q_FULL, Q_EMPTY, K_FULL, K_EMPTY = K_FULL + 2, V_FULL = K_EMPTY + 2, V_EM
        P_FULL = S_FULL + 4,       // [tile][buffer], one arrival of each softmax warp
        O_DONE = P_FULL + 4,       // [tile]: a product P V is in O
        O_LAST = O_DONE + 2,       // [tile]: the last one of these rows is
-       N_FULL = O_LAST + 2, N_EMPTY, DRAINED, NBAR = DRAINED + 2 };
+       N_FULL = O_LAST + 2, N_EMPTY, DRAINED,
+       V_TAIL = DRAINED + 2,      // a V tile that holds padding has landed
+       NBAR };
 // released by the issuing warps of both query tiles
 __host__ __device__ constexpr bool both_tiles(int i)
 {
@@ -163,6 +165,7 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
             }
         } else if (warp == kTma) {
             uint32_t kt_count = 0, qph = 0;  // tiles asked for; both rings advance together
+            uint32_t tph = 0;
             bool ok = true, more = true;
             while (more) {
                 const Work w(a, bx, by, bz);
@@ -192,13 +195,23 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
                         __syncwarp();
                         if (!ok) break;
                         ok = __all_sync(~0u, mbar_wait(bar + V_EMPTY + s, ph, a.err));
+                        // (the last tile of a block's, if any)
+                        const int keys = a.Tk - a.T + w.n;  // behind them is padding
+                        const bool tail = w.n < a.T && j0 + 128 > keys;
+                        uint64_t *landed = bar + (tail ? V_TAIL : V_FULL + s);
                         if (elect_one()) {
                             // asked for also after a failed wait: both rings stay in step for the drain below
-                            mbar_arrive_expect_tx(bar + V_FULL + s, L::TILE);
+                            mbar_arrive_expect_tx(landed, L::TILE);
                             for (int x = 0; x < D / 64; ++x)
-                                tma_load_4d(sm + L::V + s * L::TILE + x * 16384, &mv, bar + V_FULL + s, x * 64, hk, j0, w.b);
+                                tma_load_4d(sm + L::V + s * L::TILE + x * 16384, &mv, landed, x * 64, hk, j0, w.b);
                         }
                         __syncwarp();
+                        if (tail) {
+                            ok = __all_sync(~0u, mbar_wait(landed, tph, a.err)) && ok;
+                            tph ^= 1;
+                            zero_rows<D>(sm + L::V + s * L::TILE, keys - j0);
+                            if (lane == 0) mbar_arrive(bar + V_FULL + s);
+                        }
                     }
                 }
                 more = advance(ok);
@@ -307,6 +320,7 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
         while (more) {
             const Work w(a, bx, by, bz);
             const int row = w.i0 + t * 128 + r, p = a.Tk - a.T + row;
+            const bool live = row < w.n;  // (what the rows behind hold must not decide for the warp)
             float m = -INFINITY, l = 0.f;
             bool started = false;
             if (w.i0 < w.n) {
@@ -339,11 +353,11 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
                         }
                     };
                     const bool full = visits.full(j);
-                    bool careful = !full || __any_sync(~0u, m == -INFINITY);
+                    bool careful = !full || __any_sync(~0u, live && m == -INFINITY);
                     take_scores();
                     if (__builtin_expect(!careful, 1)) {
                         exponentials(m);
-                        careful = __any_sync(~0u, !((sum[0] + sum[1]) + (sum[2] + sum[3]) < kMaxSum));
+                        careful = __any_sync(~0u, live && !((sum[0] + sum[1]) + (sum[2] + sum[3]) < kMaxSum));
                         if (__builtin_expect(careful, 0)) take_scores();
                     }
                     if (__builtin_expect(careful, 0)) {
@@ -401,7 +415,7 @@ fwd_tc_kernel(const __grid_constant__ SwaArgs a, const __grid_constant__ CUtenso
                 tc_fence_after();
             }
             if (ok) {
-                const bool live = row < w.n, inside = row < a.T;
+                const bool inside = row < a.T;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 bf16 *dst = static_cast<bf16 *>(a.out) + (((long long)w.b * a.T + row) * a.Hq + w.h) * D;
                 bool bad = false;

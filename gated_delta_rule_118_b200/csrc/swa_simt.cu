@@ -166,13 +166,14 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
         load_rows<E, D, 64>(Qs, q, i0, n);
         const int p0 = off + i0, p1 = off + min(i0 + 64, n) - 1;
         const KeyTiles kt(p0, p1, a.window, a.sinks, 64);
-        if (AHEAD) ask_rows<E, D, 64>(Ks, k, kt.tile(0) * 64, a.Tk);
+        const int keys = off + n;  // behind them is padding: zeros in the tile
+        if (AHEAD) ask_rows<E, D, 64>(Ks, k, kt.tile(0) * 64, keys);
         rows_asked();
         for (int c = 0; c < kt.count(); ++c) {
             const int j0 = kt.tile(c) * 64;
             __syncthreads();
-            if (AHEAD) ask_rows<E, D, 64>(Vs, v, j0, a.Tk);
-            else ask_rows<E, D, 64>(Ks, k, j0, a.Tk);
+            if (AHEAD) ask_rows<E, D, 64>(Vs, v, j0, keys);
+            else ask_rows<E, D, 64>(Ks, k, j0, keys);
             rows_asked();
             rows_landed<AHEAD>();
             __syncthreads();
@@ -202,8 +203,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const SwaArgs a)
                 for (int u = 0; u < D / 16; ++u) o[i][u] *= f;
             }
             __syncthreads();
-            if (!AHEAD) ask_rows<E, D, 64>(Vs, v, j0, a.Tk);
-            else if (c + 1 < kt.count()) ask_rows<E, D, 64>(Ks, k, kt.tile(c + 1) * 64, a.Tk);
+            if (!AHEAD) ask_rows<E, D, 64>(Vs, v, j0, keys);
+            else if (c + 1 < kt.count()) ask_rows<E, D, 64>(Ks, k, kt.tile(c + 1) * 64, keys);
             rows_asked();
             rows_landed<AHEAD>();
             __syncthreads();
@@ -260,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const SwaArgs a)
         auto ask = [&](int c) {
             if (c < kt.count()) {
                 float *to = tiles + (AHEAD ? c & 1 : 0) * 64 * LD;
-                ask_rows<E, D, 32>(to, k, kt.tile(c) * 32, a.Tk);
-                ask_rows<E, D, 32>(to + 32 * LD, v, kt.tile(c) * 32, a.Tk);
+                ask_rows<E, D, 32>(to, k, kt.tile(c) * 32, off + n);  // (padding arrives as zeros)
+                ask_rows<E, D, 32>(to + 32 * LD, v, kt.tile(c) * 32, off + n);
             }
             rows_asked();
         };

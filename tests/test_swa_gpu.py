@@ -88,6 +88,29 @@ def test_ragged_lengths_with_garbage_in_the_padding(dtype, d):
             assert (got[n][b, lens[b]:] == 0).all(), n
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,Tk,Hq,Hk,d,W,S", [(5, 700, 700, 16, 4, 128, 200, 3), (5, 700, 700, 16, 4, 64, 1000, 0),
+                                                (4, 300, 500, 12, 2, 128, 64, 130), (3, 130, 130, 2, 1, 64, 5, 2)])
+def test_padding_that_is_not_finite_changes_no_bit(B, T, Tk, Hq, Hk, d, W, S, dtype):
+    """No row of a sequence is formed again, or by another rounding, for what its padding holds."""
+    q, k, v, dO = make(B, T, Tk, Hq, Hk, d, dtype, seed=B + d)
+    n = [T, T // 2 + 1, 1, 0, T - 2][:B]
+    lens = torch.tensor(n, dtype=torch.int32, device="cuda")
+    runs = []
+    for fill in (0.0, float("nan"), float("inf"), torch.finfo(dtype).max):
+        for b in range(B):
+            for t in (q, k, v, dO):
+                t[b, t.shape[1] - T + n[b]:] = fill
+        o, lse = g.gdn2_swa_fwd(q, k, v, lens, window=W, sinks=S)
+        runs.append(dict(o=o, lse=lse, **g.gdn2_swa_bwd(q, k, v, o, lse, dO, lens, window=W, sinks=S)))
+    assert g.gdn2_check_device_error() == g.GDN2_OK
+    ref, tol = hybrid.swa(q, k, v, lens, None, window=W, sinks=S, scale=d ** -0.5, u=U[dtype])
+    close(runs[0]["o"], ref["o"].nan_to_num(0), tol["o"].nan_to_num(0), "o")
+    for got in runs[1:]:
+        for name in got:
+            assert torch.equal(got[name], runs[0][name]), name
+
+
 def test_lengths_outside_the_range_are_cut():
     q, k, v, dO = make(2, 70, 70, 2, 2, 64, BF, seed=6)
     lens = torch.tensor([-5, 1000], dtype=torch.int32, device="cuda")
