@@ -8,10 +8,10 @@
 // column sums stay in registers.  Rows are fetched ahead into a ring in shared memory by
 // bulk copies (rows whose length is not a multiple of 8 by plain loads): the row sums of
 // one row (two in the forward, three in the backward) would otherwise leave the memory
-// idle.  Bound by HBM: 32768 x 2048 bf16 with a gate, forward 114 us (5.9 TB/s), backward
-// 213 us (5.1; three CTAs an SM, with the column sums in shared memory to fit their
+// idle.  Bound by HBM: 32768 x 2048 bf16 with a gate, forward 112 us (6.0 TB/s), backward
+// 214 us (5.0; three CTAs an SM, with the column sums in shared memory to fit their
 // registers, leave room for fewer rows fetched ahead: 226 us).  Long rows are bound by the
-// exchange of their sums: 8192 x 8192 forward 149 us (4.5 TB/s), backward 352 (3.1).
+// exchange of their sums: 8192 x 8192 forward 151 us (4.4 TB/s), backward 359 (3.0).
 //
 // The backward's sums over rows (for the three vectors' gradients) are added in a fixed
 // order: each CTA over its rows, then a small kernel over the CTAs.  dw_post and
@@ -80,6 +80,13 @@ struct Ring {
             if (src[k])
                 sm100::bulk_load(data + (st * NT + k) * tensor_bytes, static_cast<const E *>(src[k]) + n * D + c0, bytes,
                                  full + st);
+    }
+    // this stage's row is here (false: the wait gave up)
+    __device__ __forceinline__ bool wait(unsigned int *err) const { return sm100::mbar_wait(full + s, ph, err); }
+    // (one thread) everything asked for has landed, or its wait given up
+    __device__ __forceinline__ void drain(unsigned int *err)
+    {
+        for (int i = 0; i < stages; ++i, next()) (void)wait(err);
     }
     __device__ __forceinline__ const uint8_t *slot(int k) const { return data + (s * NT + k) * tensor_bytes; }
     __device__ __forceinline__ void next()
@@ -150,7 +157,7 @@ __device__ __forceinline__ f2 bounded(f2 e)
 
 // Sums of N values over the CTA (NW warps at most; absent ones leave zeros), and over
 // the cluster with CL, left in every thread.  Slots alternate, so the next sum may start
-// while slower threads still read this one.
+// while slower threads still read this one.  False in a thread whose wait gave up.
 template <int NW>
 struct SumSlots {
     alignas(16) float warp[2][2][NW];  // [slot][value][warp]
@@ -174,7 +181,7 @@ struct RowSums {
         if constexpr (CL) cg::this_cluster().sync();  // every CTA has started, its barriers set up
     }
     template <int N>
-    __device__ __forceinline__ void operator()(float (&v)[N])
+    __device__ __forceinline__ bool operator()(float (&v)[N])
     {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -210,7 +217,7 @@ struct RowSums {
                 sm100::st_async_16(sm100::peer_smem(&sl.cta[slot][rank], threadIdx.x), mine,
                                    sm100::peer_smem(sl.landed + slot, threadIdx.x));
             }
-            sm100::mbar_wait(sl.landed + slot, ph, err);
+            if (__builtin_expect(!sm100::mbar_wait(sl.landed + slot, ph, err), 0)) return false;
             f2 t = 0;
             for (int c = 0; c < size; ++c) t = add2(t, sl.cta[slot][c].x);
             const float2 u = unpack2(t);
@@ -219,8 +226,19 @@ struct RowSums {
             if (slot) ph ^= 1;
         }
         slot ^= 1;
+        return true;
     }
 };
+
+// A thread whose wait gave up leaves the kernel (barriers do not count threads that have left;
+// what it no longer asks for, sends or signals lets the others' waits give up in turn), once
+// the rows it asked for have landed and no sum is on its way to its CTA.
+template <bool VEC, bool CL, typename R>
+__device__ __forceinline__ void leave(R &ring, unsigned int *err)
+{
+    if (VEC && threadIdx.x == 0) ring.drain(err);
+    if (CL) sm100::leave_cluster();
+}
 
 // CTAs of an SM that the register budget is set for: short rows have many small CTAs.
 constexpr int fwd_ctas(int nw) { return nw == 1 ? 24 : nw == 4 ? 8 : nw == 8 ? 4 : 2; }
@@ -284,7 +302,7 @@ __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const N
     for (long long n = first; n < a.N; n += step) {
         if constexpr (VEC) {
             const bool on = c0 + tid * 8 < cols;
-            sm100::mbar_wait(full + ring.s, ring.ph, a.err);
+            if (__builtin_expect(!ring.wait(a.err), 0)) return leave<VEC, CL>(ring, a.err);
             y.from_ring(ring.slot(0), tid, on);
             r.from_ring(ring.slot(1), tid, on);
             g.from_ring(ring.slot(2), tid, on);
@@ -303,7 +321,7 @@ __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const N
             sq = fma2(yv[i], yv[i], sq);
         }
         float s[1] = {sum2(sq)};
-        sums(s);
+        if (__builtin_expect(!sums(s), 0)) return leave<VEC, CL>(ring, a.err);
         if constexpr (VEC) {  // every thread has its columns: the slot takes the row `stages` ahead
             if constexpr (NW == 1) __syncwarp();
             if (tid == 0 && n + stages * step < a.N) ring.fetch(ring.s, n + stages * step, a.D, c0, cols);
@@ -318,7 +336,7 @@ __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const N
         }
         store_eight<E, VEC>(static_cast<E *>(a.r_out) + n * a.D, r1, c0, tid, nt, cols);
         s[0] = sum2(sq);
-        sums(s);
+        if (__builtin_expect(!sums(s), 0)) return leave<VEC, CL>(ring, a.err);
         const f2 ir = both(rsqrtf(fmaf(s[0], rd, a.eps)));
         f2 wq[4];
         take_eight<VEC>(wq, vec + cols - c0, tid, nt, cols - c0);
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(32 * NW, fwd_ctas(NW)) norm_fwd_kernel(const N
         for (int i = 0; i < 4; ++i) r1[i] = mul2(r1[i], mul2(ir, wq[i]));
         store_eight<E, VEC>(static_cast<E *>(a.x_out) + n * a.D, r1, c0, tid, nt, cols);
     }
-    // (no CTA leaves before all values sent to it have landed: it waits for each of its sums)
+    // (nothing is on its way to a CTA here: it has waited for each of its sums and rows)
 }
 
 template <typename E, bool VEC, bool CL, int NW>
@@ -359,7 +377,7 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
     for (long long n = first; n < a.N; n += step) {
         if constexpr (VEC) {
             const bool on = c0 + tid * 8 < cols;
-            sm100::mbar_wait(full + ring.s, ring.ph, a.err);
+            if (__builtin_expect(!ring.wait(a.err), 0)) return leave<VEC, CL>(ring, a.err);
             y.from_ring(ring.slot(0), tid, on);
             r.from_ring(ring.slot(1), tid, on);
             g.from_ring(ring.slot(2), tid, on);
@@ -388,7 +406,7 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             for (int i = 0; i < 4; ++i) ge[i] = bounded(ge[i]);
         }
         float s[1] = {sum2(sq)};
-        sums(s);
+        if (__builtin_expect(!sums(s), 0)) return leave<VEC, CL>(ring, a.err);
         if constexpr (VEC) {  // every thread has its columns: the slot takes the row `stages` ahead
             if constexpr (NW == 1) __syncwarp();
             if (tid == 0 && n + stages * step < a.N) ring.fetch(ring.s, n + stages * step, a.D, c0, cols);
@@ -408,7 +426,7 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             sx = fma2(wx[i], r1[i], sx);
         }
         float q[2] = {sum2(sq), sum2(sx)};
-        sums(q);
+        if (__builtin_expect(!sums(q), 0)) return leave<VEC, CL>(ring, a.err);
         const float irs = rsqrtf(fmaf(q[0], rd, a.eps));
         const f2 ir = both(irs), mx = both(-q[1] * rd * irs * irs);
         sq = 0;
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
         }
         store_eight<E, VEC>(static_cast<E *>(a.dr) + n * a.D, dv, c0, tid, nt, cols);
         s[0] = sum2(sq);
-        sums(s);
+        if (__builtin_expect(!sums(s), 0)) return leave<VEC, CL>(ring, a.err);
         const f2 my = both(-s[0] * rd);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

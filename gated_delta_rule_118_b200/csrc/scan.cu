@@ -90,16 +90,19 @@ struct Maps {
     ulonglong2 cta[2][kMaxCluster][32];   // [parity][CTA][lane]
     uint64_t landed[2];                   // [parity]: every CTA's map is here
 };
-// From this warp's map and the running state: the state entering its span; `state`
+// From this warp's map and the running state: the state `in` entering its span; `state`
 // becomes the one behind the whole cluster's span.  `order` is the warp's (or the CTA's)
-// position along the walk.
+// position along the walk.  `ok`: this thread's waits so far; false for the whole CTA, which
+// then ends its walk, if one of them gave up before this step (one that gives up in this step
+// leaves ok false in its thread).
 template <bool CL>
-__device__ __forceinline__ f2 enter_span(Maps &m, int step, int order, f2 A, f2 H, f2 &state, unsigned int *err)
+__device__ __forceinline__ bool enter_span(Maps &m, int step, int order, f2 A, f2 H, f2 &state, f2 &in, bool &ok, unsigned int *err)
 {
     const int parity = step & 1;
     const int lane = threadIdx.x & 31;
     m.warp[parity][order][lane] = make_ulonglong2(A, H);
-    __syncthreads();
+    ok = __syncthreads_and(ok);
+    if (!ok) return false;
     f2 pa = both(1.f), ph = 0, ta = both(1.f), th = 0;  // before this warp, and in all
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -108,7 +111,7 @@ __device__ __forceinline__ f2 enter_span(Maps &m, int step, int order, f2 A, f2 
         ta = mul2(v.x, ta);
         th = fma2(v.x, th, v.y);
     }
-    f2 in = state;
+    in = state;
     if constexpr (CL) {
         // each CTA sends its map to all and waits for theirs: 16 bytes a lane that signal the
         // receiver's barrier (1 x 65536 x 2048 bf16: 245 us, against 332 us with a barrier of
@@ -120,7 +123,7 @@ __device__ __forceinline__ f2 enter_span(Maps &m, int step, int order, f2 A, f2 
         for (int p = order; p < size; p += kWarps)
             sm100::st_async_16(sm100::peer_smem(&m.cta[parity][rank][lane], p), make_ulonglong2(ta, th),
                                sm100::peer_smem(m.landed + parity, p));
-        sm100::mbar_wait(m.landed + parity, (step >> 1) & 1, err);
+        ok = sm100::mbar_wait(m.landed + parity, (step >> 1) & 1, err);
         f2 s = state;
         for (int r = 0; r < size; ++r) {
             if (r == rank) in = s;
@@ -131,7 +134,8 @@ __device__ __forceinline__ f2 enter_span(Maps &m, int step, int order, f2 A, f2 
     } else {
         state = fma2(ta, state, th);
     }
-    return fma2(pa, in, ph);
+    in = fma2(pa, in, ph);
+    return true;
 }
 
 // Where a CTA works: channels, batch, and its place among the CTAs of its span.
@@ -163,6 +167,16 @@ __device__ __forceinline__ void fetch_span(uint8_t *st, const SpanMaps &m, uint6
     sm100::tma_load_2d(st + S::LA, &m.la, bar, c, (int)row);
 #pragma unroll
     for (int k = 0; k < NE; ++k) sm100::tma_load_2d(st + S::el(k), &m.e[k], bar, c, (int)row);
+}
+
+// (one thread) waits for the stages that hold the next `left` spans, at most all of them.
+template <int COUNT>
+__device__ __forceinline__ void drain(uint64_t *full, int st, uint32_t ph, long long left, unsigned int *err)
+{
+    for (int i = 0; i < COUNT && i < left; ++i) {
+        (void)sm100::mbar_wait(full + st, ph, err);
+        if (++st == COUNT) st = 0, ph ^= 1;
+    }
 }
 
 // Token t (of the warp's 16) of a tensor: from the stage, or from memory.
@@ -201,12 +215,14 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read h0, which h_T may alias)
     int k = 0, st = 0;
     uint32_t ph = 0;
-    for (long long s0 = 0; s0 < a.T; s0 += step, ++k) {
+    bool ok = true;
+    long long s0 = 0;
+    for (; s0 < a.T; s0 += step, ++k) {
         const long long t0 = s0 + pl.rank * kSpan + warp * kTok;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
         const long long row = (seq + t0) * a.C;
         const uint8_t *tile = dyn + st * S::BYTES;
-        if (SRC == kTile) sm100::mbar_wait(full + st, ph, a.err);
+        if (SRC == kTile) ok = sm100::mbar_wait(full + st, ph, a.err) && ok;
         f2 al[kTok], u[kTok], A = both(1.f), H = 0;
         auto gather = [&](auto whole) {
 #pragma unroll
@@ -225,7 +241,8 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
             A = mul2(al[t], A);
             H = fma2(al[t], H, u[t]);
         }
-        f2 h = enter_span<CL>(maps, k, warp, A, H, state, a.err);
+        f2 h;
+        if (!enter_span<CL>(maps, k, warp, A, H, state, h, ok, a.err)) break;
         if (SRC == kTile) {  // (behind the barrier of enter_span: every warp has its tokens in registers)
             if (threadIdx.x == 0 && s0 + S::COUNT * step < a.T)
                 fetch_span<E, 2>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + s0 + S::COUNT * step + pl.rank * kSpan);
@@ -239,6 +256,12 @@ scan_fwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
             if (t < live) store_pair<EVEN>(y, c, a.C, h);
             y += a.C;
         }
+    }
+    if (__builtin_expect(!ok, 0)) {
+        // a wait gave up: the tiles asked for have landed, and no map is on its way, before the CTA ends
+        if (SRC == kTile && threadIdx.x == 0) drain<S::COUNT>(full, st, ph, s0 < a.T ? (a.T - 1 - s0) / step + 1 : 0, a.err);
+        if (CL) sm100::leave_cluster();
+        return;
     }
     if (a.h_T && warp == 0 && pl.rank == 0) store_pair<EVEN>(a.h_T + (long long)pl.b * a.C, c, a.C, state);
 }
@@ -276,7 +299,9 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
     if constexpr (CL) cg::this_cluster().sync();  // every CTA has started (and read dh_T, which dh0 may alias)
     int k = 0, st = 0;
     uint32_t ph = 0;
-    for (long long sp = spans - 1; sp >= 0; --sp, ++k) {
+    bool ok = true;
+    long long sp = spans - 1;
+    for (; sp >= 0; --sp, ++k) {
         const int wrow = (kWarps - 1 - warp) * kTok;
         const long long t0 = first_token(sp) + wrow;
         const int live = t0 >= a.T ? 0 : a.T - t0 < kTok ? (int)(a.T - t0) : kTok;
@@ -284,7 +309,7 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         const E *x = static_cast<const E *>(a.x) + row, *w = static_cast<const E *>(a.w) + row, *dy = static_cast<const E *>(a.dy) + row;
         const uint8_t *tile = dyn + st * S::BYTES;
         f2 h = live ? load_pair<EVEN>(a.ckpt + ((long long)pl.b * nblk + t0 / kTok) * a.C, c, a.C) : 0;
-        if (SRC == kTile) sm100::mbar_wait(full + st, ph, a.err);
+        if (SRC == kTile) ok = sm100::mbar_wait(full + st, ph, a.err) && ok;
         // x, w and dy are taken twice (from the stage, or from cache): kept in registers they
         // would halve the warps of an SM
         auto get = [&](int k, const E *p, int t) { return take<SRC>(tile + S::el(k), p, wrow, t, c, a.C); };
@@ -306,7 +331,8 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
         };
         if (live == kTok) gather(std::true_type());
         else gather(std::false_type());
-        f2 g = enter_span<CL>(maps, k, warp, A, G, state, a.err);
+        f2 g;
+        if (!enter_span<CL>(maps, k, warp, A, G, state, g, ok, a.err)) break;
         E *dx = static_cast<E *>(a.dx) + row, *dw = static_cast<E *>(a.dw) + row;
         float *dla = a.dla + row;
         auto sweep = [&](auto whole) {
@@ -327,11 +353,18 @@ scan_bwd_kernel(const ScanArgs a, int csize, const __grid_constant__ SpanMaps tm
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(empty + st);
             if (threadIdx.x == 0 && sp >= S::COUNT) {
-                sm100::mbar_wait(empty + st, ph, a.err);
-                fetch_span<E, 3>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + first_token(sp - S::COUNT));
+                if (sm100::mbar_wait(empty + st, ph, a.err))
+                    fetch_span<E, 3>(dyn + st * S::BYTES, tm, full + st, c_cta, seq + first_token(sp - S::COUNT));
+                else
+                    ok = false;
             }
             if (++st == S::COUNT) st = 0, ph ^= 1;
         }
+    }
+    if (__builtin_expect(!ok, 0)) {
+        if (SRC == kTile && threadIdx.x == 0) drain<S::COUNT>(full, st, ph, sp + 1, a.err);
+        if (CL) sm100::leave_cluster();
+        return;
     }
     if (a.dh0 && warp == 0 && pl.rank == 0) store_pair<EVEN>(a.dh0 + (long long)pl.b * a.C, c, a.C, state);
 }

@@ -231,6 +231,19 @@ __device__ __forceinline__ void st_async_16(uint32_t addr, ulonglong2 v, uint32_
                  : "memory");
 }
 
+// For a thread whose wait gave up, before it leaves a kernel whose CTAs store into each
+// other's shared memory: waits until every other thread of the cluster has left or has come
+// here as well (threads that have left are not waited for), so that nothing more is sent to
+// this CTA, and then until what was sent last has landed (a tenth of a millisecond, where a
+// store takes a microsecond).  Every other wait being bounded, all of them do leave or come.
+__device__ __forceinline__ void leave_cluster()
+{
+    asm volatile(
+        "barrier.cluster.arrive.release;\n\t"
+        "barrier.cluster.wait.acquire;\n\t"
+        "nanosleep.u32 100000;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- cluster launch control
 // Ask for a CTA of this grid that has not started yet, to run its work here instead:
 // 16 bytes arrive in `response` and complete on `bar` (after mbar_arrive_expect_tx of
