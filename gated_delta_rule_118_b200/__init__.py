@@ -278,15 +278,39 @@ def gdn2_decode_tokens(q, k, v, b, w, log_alpha, S, o=None, *, stream=None, chec
 _caller = None
 
 
+_CALLS = ("gdn2_swa_fwd", "gdn2_swa_bwd", "gdn2_swa_decode", "gdn2_scan_fwd", "gdn2_scan_bwd", "gdn2_scan_step",
+          "gdn2_block_norm_fwd", "gdn2_block_norm_bwd")
+
+
+class _Ctypes:
+    """The calls of module _call, through ctypes (2 to 4 microseconds more a call)."""
+
+    def __init__(self, L):
+        for name in _CALLS:
+            setattr(self, name[len("gdn2_"):], self._of(getattr(L, name)))
+
+    @staticmethod
+    def _of(fn):
+        sizes = [i for i, t in enumerate(fn.argtypes) if t is ctypes.c_int]
+
+        def call(*args):
+            if any(not -2 ** 31 <= args[i] < 2 ** 31 for i in sizes):  # (ctypes would cut it)
+                raise OverflowError("a size does not fit 32 bits")
+            return fn(*((ctypes.c_longlong * len(a))(*a) if isinstance(a, tuple) else a for a in args))
+        return call
+
+
 def _native():
-    """The module that calls libgdn2.so for the functions below (built with it)."""
+    """What calls libgdn2.so for the functions below: the module built with it, else ctypes."""
     global _caller
     if _caller is None:
         L = lib()
-        from . import _call as module
-        names = ("gdn2_swa_fwd", "gdn2_swa_bwd", "gdn2_swa_decode", "gdn2_scan_fwd", "gdn2_scan_bwd", "gdn2_scan_step",
-                 "gdn2_block_norm_fwd", "gdn2_block_norm_bwd")
-        module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        try:
+            from . import _call as module
+        except ImportError:
+            module = _Ctypes(L)
+        else:
+            module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CALLS))
         _caller = module
     return _caller
 

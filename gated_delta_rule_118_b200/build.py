@@ -1,11 +1,13 @@
-"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a, and the Python
-module that calls it (_call.so) with the host compiler."""
+"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a, and with the host
+compiler the Python module that calls it with less overhead than ctypes (_call, one
+file an interpreter; the library serves without it)."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -13,7 +15,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libgdn2.so"
-CALLER = PKG / "_call.so"
+CALLER = PKG / f"_call{sysconfig.get_config_var('EXT_SUFFIX')}"  # (the interpreter's own: its version is in the name)
 OBJDIR = PKG / "_build"
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -30,21 +32,46 @@ def sources() -> list[Path]:
     return sorted(CSRC.glob("*.cu"))
 
 
-def _deps() -> list[Path]:
-    return sources() + sorted(CSRC.glob("*.c")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h"))
+def _older(built: Path, deps: list[Path]) -> bool:
+    return not built.exists() or any(p.stat().st_mtime > built.stat().st_mtime for p in deps)
 
 
 def is_stale() -> bool:
-    if not LIBRARY.exists() or not CALLER.exists():
-        return True
-    t = min(LIBRARY.stat().st_mtime, CALLER.stat().st_mtime)
-    return any(p.stat().st_mtime > t for p in _deps())
+    """Whether libgdn2.so is missing or older than its sources."""
+    return _older(LIBRARY, sources() + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h")))
+
+
+def build_caller(force: bool = False) -> Path:
+    """Compile csrc/binding.c for this interpreter; raises RuntimeError where that cannot be done."""
+    if not force and not _older(CALLER, [CSRC / "binding.c", *INCLUDE.glob("*.h")]):
+        return CALLER
+    tmp = CALLER.with_suffix(".tmp")
+    host = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall", "-Wno-unused-parameter",
+            f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", str(CSRC / "binding.c"), "-o", str(tmp)]
+    try:
+        r = subprocess.run(host, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{host[0]} cannot be run: {e}") from e
+    if r.returncode != 0:
+        raise RuntimeError(f"{host[0]} failed on binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLER)
+    return CALLER
 
 
 def build_library(force: bool = False, verbose: bool = False) -> Path:
-    """Compile every csrc/*.cu to an object and link them into libgdn2.so; compile _call.so."""
-    if not force and not is_stale():
-        return LIBRARY
+    """Compile every csrc/*.cu to an object and link them into libgdn2.so; then compile the calling
+    module, without which (no host compiler, no headers of Python) the library is as good, only its
+    calls from Python take some microseconds longer."""
+    if force or is_stale():
+        _build_library(verbose)
+    try:
+        build_caller(force)
+    except RuntimeError as e:
+        warnings.warn(f"the hybrid block's operators are called through ctypes: {e}")
+    return LIBRARY
+
+
+def _build_library(verbose: bool) -> None:
     OBJDIR.mkdir(exist_ok=True)
     objs = []
     procs = []
@@ -65,18 +92,10 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    caller = CALLER.with_suffix(".so.tmp")
-    host = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall", "-Wno-unused-parameter",
-            f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", str(CSRC / "binding.c"), "-o", str(caller)]
-    r = subprocess.run(host, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{host[0]} failed on binding.c:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
-    os.replace(caller, CALLER)
     (OBJDIR / "ptxas.log").write_text("\n".join(logs))
     if verbose:
         print("\n".join(logs))
-    return LIBRARY
 
 
 if __name__ == "__main__":
