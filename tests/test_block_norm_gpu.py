@@ -41,6 +41,25 @@ def test_shapes(shape, gate, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("shape", [(5000, 96), (700, 2048), (2500, 1001), (900, 5120), (300, 8200), (60, 16384)])
+def test_errors_in_the_mean_square(shape, gate, dtype):
+    """Beside the bounds of each element, which grow with the length of a row and the number of rows: sums
+    whose terms have no common sign, in trees and chains of at most about 100 fp32 roundings, stay within
+    100 * 2^-24 = 6e-6 in the mean square; what is written in the type has its own rounding besides."""
+    args, dr, dx = make(shape, dtype, gate, seed=sum(shape) + 1)
+    r_out, x_out = g.gdn2_block_norm_fwd(*args, EPS)
+    got = {"r_out": r_out, "x_out": x_out, **g.gdn2_block_norm_bwd(*args, dr, dx, EPS)}
+    ref, _ = hybrid.block_norm(*args, EPS, dr, dx, u=U[dtype])
+    for n, t in got.items():
+        if t is None:
+            continue
+        own = U[dtype] / 3 ** 0.5 if t.dtype == BF else 0.0
+        err = (t.double() - ref[n]).norm() / ref[n].norm()
+        assert err <= own * 1.01 + 1e-5, (n, err)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_tiny_rows_large_rows_and_strong_gates(dtype):
     args, dr, dx = make((6, 512), dtype, True, seed=1)
     args[0][0] = args[1][0] = 0          # a row of zeros: eps alone

@@ -38,6 +38,14 @@ def test_shapes(B, T, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("C", [1024, 1030, 1001])
+@pytest.mark.parametrize("T", [337, 64])
+def test_a_cta_walks_over_several_spans_by_itself(T, C, dtype):
+    """As many channel tiles as SMs and more: no clusters, and more spans than tiles are fetched ahead."""
+    check(*make(10, T, C, dtype, seed=T + C))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_strong_decay_resets_and_no_state(dtype):
     x, w, la, h0, dy, dh = make(2, 300, 68, dtype, seed=1, strong=True)
     la[:, 100] = -float("inf")   # a new document: nothing before it remains

@@ -294,6 +294,72 @@ def test_other_stream_and_captured_graph(dtype):
     assert torch.equal(o, o3) and all(torch.equal(ref[n], got[n]) for n in ref)
 
 
+@pytest.mark.parametrize("Hk,d,W,S", [(8, 64, 300, 3), (32, 128, 1000, 0)])
+def test_more_blocks_than_the_device_holds_at_once(Hk, d, W, S):
+    """480 blocks of 256 rows, full ones, short ones and padding: a CTA of the forward takes several, and
+    carries its rings, score buffers and phases from one to the next."""
+    B, T, Hq = 5, 700, 32
+    q, k, v, dO = make(B, T, T, Hq, Hk, d, BF, seed=d)
+    lens = torch.tensor([700, 300, 0, 257, 513], dtype=torch.int32, device="cuda")
+    check(q, k, v, dO, lens, W, S)
+    o, lse = g.gdn2_swa_fwd(q, k, v, window=W, sinks=S)
+    for b in (1, 3):  # rows do not depend on what else the batch holds
+        one, lse1 = g.gdn2_swa_fwd(q[b:b + 1], k[b:b + 1], v[b:b + 1], window=W, sinks=S)
+        assert torch.equal(o[b:b + 1], one) and torch.equal(lse[b:b + 1], lse1)
+
+
+@pytest.mark.parametrize("B,T,Tk,Hq,Hk,d,W,S,ragged", [(1, 2300, 2300, 2, 1, 64, 200, 4, False), (2, 2300, 2300, 2, 2, 128, 300, 260, True),
+                                                       (1, 4500, 4500, 2, 1, 64, 500, 4, False), (1, 4500, 4700, 2, 1, 128, 128, 260, True)])
+def test_query_segments_of_the_sinks(B, T, Tk, Hq, Hk, d, W, S, ragged):
+    """More than 16 query tiles and sinks: the sinks' queries are split into segments, whose partial sums
+    another kernel adds; and its rows that are not finite are formed again."""
+    q, k, v, dO = make(B, T, Tk, Hq, Hk, d, BF, seed=T + S)
+    lens = torch.tensor([T - 150, T // 3][:B], dtype=torch.int32, device="cuda") if ragged else None
+    base = check(q, k, v, dO, lens, W, S)
+    again = g.gdn2_swa_bwd(q, k, v, base["o"], base["lse"], dO, lens, window=W, sinks=S)
+    assert all(torch.equal(base[n], again[n]) for n in again)
+    row = T // 3 - 7
+    dO[0, row] = float("nan")
+    got = g.gdn2_swa_bwd(q, k, v, base["o"], base["lse"], dO, lens, window=W, sinks=S)
+    seen = hybrid.visible(T, Tk, W, S, "cuda")[row]
+    assert seen[:S].all() and not seen[S:128].any()  # (the sinks' tile holds keys of both kinds)
+    for n in ("dk", "dv"):
+        assert got[n][0, seen].isnan().any(-1).all() and got[n][0, ~seen].isfinite().all(), n
+        a, b = got[n][0, ~seen].float(), base[n][0, ~seen].float()
+        assert ((a - b).abs() <= 0.03 * b.abs().max()).all(), n
+
+
+def test_long_segments_of_the_sinks():
+    """So many query tiles that segments are longer than 16 of them: the sinks' dk and dv against fp64 sums
+    over all rows, with the probabilities formed from the forward's lse."""
+    T, d, W, S = 40_000, 64, 128, 4
+    q, k, v, dO = make(1, T, T, 1, 1, d, BF, seed=31)
+    o, lse = g.gdn2_swa_fwd(q, k, v, window=W, sinks=S)
+    got = g.gdn2_swa_bwd(q, k, v, o, lse, dO, window=W, sinks=S)
+    Q, K, V, G, O = (t[0, :, 0].double() for t in (q, k, v, dO, o))
+    see = torch.arange(T, device="cuda")[:, None] >= torch.arange(S, device="cuda")[None]
+    p = torch.where(see, torch.exp(Q @ K[:S].T * d ** -0.5 - lse[0, 0].double()[:, None]), 0.0)
+    dS = p * (G @ V[:S].T - (G * O).sum(-1, keepdim=True))
+    # P is rounded by at most 2^-8 of itself for dv, independently row by row, and so the sum's error is at
+    # most 2^-8 of the sum in the mean square; the output's rounding is another 2^-8
+    for n, ref in (("dv", p.T @ G), ("dk", dS.T @ Q * d ** -0.5)):
+        assert (got[n][0, :S, 0].double() - ref).norm() <= 2.0 ** -7 * ref.norm(), n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_later_keys_that_outgrow_the_first_tiles_by_far(d):
+    """Scores that jump by 2^90 and by more than fp32 holds between blocks all of whose keys are visible:
+    those blocks are taken again with a new reference."""
+    T = 900
+    q, k, v, dO = make(1, T, T, 2, 1, d, BF, seed=32, scale=0.3)
+    q[..., 0] = 8.0
+    for j, level in ((0, 0.0), (130, 8.0), (330, 12.0), (520, 40.0), (700, 3.0)):  # scores of 0, 64, 96, 320, 24
+        k[:, j:, :, 0] = level
+    for lens in (None, torch.tensor([610], dtype=torch.int32, device="cuda")):
+        check(q, k, v, dO, lens, T, 0, scale=1.0)
+        check(q, k, v, dO, lens, 512, 70, scale=1.0)
+
+
 # ---------------------------------------------------------------- decode
 def decode_case(B, slots, Hq, Hk, d, dtype, seed):
     gen = torch.Generator("cuda").manual_seed(seed)
@@ -317,6 +383,18 @@ def test_decode(Hq, Hk, d, window, sinks, extra, dtype):
     slots = window + sinks + extra
     pos = torch.tensor([0, 1, sinks, slots - 1, slots, 2 * slots + 3, -1, 1_000_003], dtype=torch.int32, device="cuda")
     q, k, v, kc, vc = decode_case(len(pos), slots, Hq, Hk, d, dtype, seed=Hq + window)
+    check_decode(q, k, v, kc, vc, pos, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 5, 8, 12])
+@pytest.mark.parametrize("B,Hk,window,sinks", [(64, 4, 300, 3), (64, 8, 50, 2)])
+def test_decode_of_a_batch(B, Hk, window, sinks, G, d, dtype):
+    """Batches that fill the device: few CTAs a row, and (the second) one, which needs no cluster."""
+    slots = window + sinks + 3
+    q, k, v, kc, vc = decode_case(B, slots, G * Hk, Hk, d, dtype, seed=G + d)
+    pos = torch.arange(B, dtype=torch.int32, device="cuda") * 37 % 800 - 1
     check_decode(q, k, v, kc, vc, pos, window, sinks)
 
 
