@@ -21,10 +21,12 @@
  *   - All tensor arguments are DEVICE pointers owned by the caller.  The
  *     library keeps no per-call state and never synchronises the stream; work
  *     is queued on `stream` (NULL = the legacy default stream) and the call
- *     returns once it is queued.  The bf16 path of gdn2_fwd_chunked needs a
- *     workspace, which it takes from a stream-ordered pool owned by the
- *     library (allocated and released on `stream`; the pool keeps freed
- *     blocks for reuse).  Nothing else allocates.
+ *     returns once it is queued.  The bf16 paths of gdn2_fwd_chunked,
+ *     gdn2_fwd_chunked_gates and gdn2_layer_fwd, and gdn2_bwd_chunked,
+ *     gdn2_swa_bwd and gdn2_block_norm_bwd, need a workspace, which they take
+ *     from a stream-ordered pool owned by the library (allocated and released
+ *     on `stream`; the pool keeps freed blocks for reuse).  Nothing else
+ *     allocates.
  *   - Layouts are dense row-major: q, k, b, log_alpha are [B][T][H][dk];
  *     v, w, o are [B][T][H][dv]; states are [B][H][dk][dv].  (The decode entry
  *     point drops the T axis.)
@@ -308,8 +310,10 @@ gdn2_status gdn2_bwd_chunked(const void *q, const void *k, const void *v,
  * diagonal gated linear recurrence, and the norms around a block.  The pages'
  * hybrid model interleaves the operator above with attention over a window of
  * 2K tokens (iplexlaw.co.kr, section "Condiciones de comparacion"; gist.science,
- * architecture).  They follow the conventions at the top of this header, with
- * one addition: the gradient of an input has the input's own type.
+ * architecture).  The recurrence and the norms with their gate and residual
+ * scale are not on the pages; they are what else a block of this kind is made
+ * of.  All follow the conventions at the top of this header, with one addition:
+ * the gradient of an input has the input's own type.
  * ======================================================================
  */
 
@@ -336,8 +340,11 @@ gdn2_status gdn2_bwd_chunked(const void *q, const void *k, const void *v,
  *               needs it)
  *   strides     host array of 9 element strides, {batch, token, head} of q, then of
  *               k, then of v; NULL means dense.  The d elements of a row are always
- *               contiguous; a stride is a multiple of 16 bytes and at least d.
- *               Strides of an axis of size 1 are ignored.
+ *               contiguous; a stride is a multiple of 16 bytes and at least d
+ *               (an axis cannot be broadcast).  Strides of an axis of size 1 are
+ *               ignored.  Rows of a view may share memory otherwise (windows that
+ *               slide over one buffer): each is read as a row of its own, and its
+ *               gradient is its own as well.
  *   d 64 or 128; Hq a multiple of Hk; 0 <= T <= Tk <= GDN2_SWA_MAX_TOKENS;
  *   window >= 1; 0 <= sinks; 1e-30 <= scale <= 1e30.
  *
@@ -403,8 +410,8 @@ gdn2_status gdn2_swa_decode(const void *q, const void *k, const void *v, void *k
  *     h_t = alpha_t h_{t-1} + w_t x_t,   alpha_t = exp(log_alpha_t),   y_t = h_t.
  *
  *   x, w        [B][T][C]  dtype   input and write gate
- *   log_alpha   [B][T][C]  fp32    log of the decay (<= 0; -infinity forgets everything
- *               before that token)
+ *   log_alpha   [B][T][C]  fp32    log of the decay (<= 0; -infinity forgets the state
+ *               before that token, if it is finite: 0 times infinity or NaN is NaN)
  *   h0          [B][C]     fp32    initial state; NULL means zero
  *   y           [B][T][C]  dtype   written
  *   h_T         [B][C]     fp32    final state; NULL means not written.  May alias h0.
@@ -451,7 +458,8 @@ gdn2_status gdn2_scan_step(const void *x, const void *w, const float *log_alpha,
  * residual stream r, and the sum is normalised for the next block.  Per row:
  *     r_out = r + res_scale (*) sigmoid(g_logit) (*) (y / rms(y)) (*) w_post
  *     x_out = (r_out / rms(r_out)) (*) w_pre          rms(a) = sqrt(mean(a^2) + eps)
- * x_out is formed from r_out before its rounding.
+ * x_out is formed from r_out before its rounding.  Sums of squares are fp32: they hold
+ * for rows whose elements stay below about 1e17.
  *
  *   r, y        [N][D]  dtype   residual stream, block output
  *   g_logit     [N][D]  dtype   gate logits; NULL means no gate (sigmoid -> 1)

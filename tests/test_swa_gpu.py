@@ -193,6 +193,23 @@ def test_strided_views_of_one_projection(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("order", ["sequences", "heads"])
+def test_views_whose_rows_share_memory(order, dtype):
+    """Windows that slide over one buffer, by a token a sequence or by a token a head: every row of the view
+    counts as its own, in the outputs and in the gradients."""
+    B, T, H, d = 3, 140, 4, 64
+    gen = torch.Generator("cuda").manual_seed(16)
+    n = (T + B + H) * H * d
+    q, k, v = (torch.randn(n, generator=gen, device="cuda").to(dtype).as_strided(
+        (B, T, H, d), (H * d, H * d, d, 1) if order == "sequences" else (T * d, d, d, 1)) for _ in range(3))
+    dO = torch.randn(B, T, H, d, generator=gen, device="cuda").to(dtype)
+    got = check(q, k, v, dO, None, 40, 2)
+    dense = check(q.contiguous(), k.contiguous(), v.contiguous(), dO, None, 40, 2)
+    for name in got:
+        assert torch.equal(got[name], dense[name]), name
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_repeated_calls_give_identical_bits(dtype):
     q, k, v, dO = make(2, 500, 500, 8, 2, 128, dtype, seed=11)
     runs = []
