@@ -9,9 +9,9 @@
 // bulk copies (rows whose length is not a multiple of 8 by plain loads): the row sums of
 // one row (two in the forward, three in the backward) would otherwise leave the memory
 // idle.  Bound by HBM: 32768 x 2048 bf16 with a gate, forward 112 us (6.0 TB/s), backward
-// 214 us (5.0; three CTAs an SM, with the column sums in shared memory to fit their
+// 213 us (5.0; three CTAs an SM, with the column sums in shared memory to fit their
 // registers, leave room for fewer rows fetched ahead: 226 us).  Long rows are bound by the
-// exchange of their sums: 8192 x 8192 forward 151 us (4.4 TB/s), backward 359 (3.0).
+// exchange of their sums: 8192 x 8192 forward 151 us (4.4 TB/s), backward 361 (3.0).
 //
 // The backward's sums over rows (for the three vectors' gradients) are added in a fixed
 // order: each CTA over its rows, then a small kernel over the CTAs.  dw_post and
@@ -405,6 +405,13 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
 #pragma unroll
             for (int i = 0; i < 4; ++i) ge[i] = bounded(ge[i]);
         }
+        // 1 - gate as e * gate: the difference has 3 % of itself left at a logit of 12, and nothing
+        // above 17.  (Formed here, or at its use where registers are short: 30000 x 1001 bf16 231
+        // us, and 249 formed here; 16384 x 4096 fp32 368 formed here, and 388 at its use.)
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ge[i] = mul2(ge[i], gt[i]);
+        }
         float s[1] = {sum2(sq)};
         if (__builtin_expect(!sums(s), 0)) return leave<VEC, CL>(ring, a.err);
         if constexpr (VEC) {  // every thread has its columns: the slot takes the row `stages` ahead
@@ -447,9 +454,7 @@ __global__ void __launch_bounds__(32 * NW, bwd_ctas(NW)) norm_bwd_kernel(const N
             const f2 b = mul2(xv[i], yv[i]), bt = mul2(b, t[i]);
             bsum[i] = add2(bsum[i], b);
             r1[i] = mul2(iy, fma2(my, yv[i], r1[i]));
-            // 1 - gate as e * gate: the difference has 3 % of itself left at a logit of 12, and
-            // nothing above 17
-            if (a.g) dv[i] = mul2(bt, mul2(ge[i], gt[i]));
+            if (a.g) dv[i] = mul2(bt, VEC ? ge[i] : mul2(ge[i], gt[i]));
         }
         store_eight<E, VEC>(static_cast<E *>(a.dy) + n * a.D, r1, c0, tid, nt, cols);
         if (a.g) store_eight<E, VEC>(static_cast<E *>(a.dg) + n * a.D, dv, c0, tid, nt, cols);

@@ -14,11 +14,14 @@
 // output tile takes every eighth channel so that a lane's 16 bytes of a value row feed
 // eight tiles.  (The fifth-generation tensor core would not be used a tenth: a step of 16
 // keys is 64 warp instructions here against 8 KB from memory.)
-// 256 sequences of 2052 positions, 16 query heads of 128 over 4: 216 us, 4.98 TB/s; over
-// 16: 755 us, 5.70 TB/s; one sequence: 11 us.  What is left of the first is the CTAs' own
-// beginning and end (position, query, first rows; join), about 10 us a wave: three CTAs of
-// an SM overlap it (with two, and twice the bytes in flight, 231 us).
-// fp32: one key row per half or whole warp on the CUDA cores.
+// 256 sequences of 2052 positions, 16 query heads of 128 over 4: 214 us (5.0 TB/s) call after
+// call in a graph, 232 with the caches of other sequences in between; over 16: 775 us, 5.6
+// TB/s; one sequence: 9 us in a graph.  Heads of 64: 113 over 4, 405 over 16.  What is left of
+// the first is the CTAs' own beginning and end (position, query, first rows; join), about 10
+// us a wave: three CTAs of an SM overlap it (with two, and twice the bytes in flight, 231 us).
+// fp32: one key row per half or whole warp on the CUDA cores, up to four heads of a group a
+// CTA; 64 sequences of 2052 positions, 8 heads of 128 over 8: 174 us (6.2 TB/s), 16 over 4: 185,
+// 32 over 4 (whose cache is read twice): 328.
 #include <cooperative_groups.h>
 
 #include "launch.h"

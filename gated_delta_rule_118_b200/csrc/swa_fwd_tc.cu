@@ -12,8 +12,8 @@
 // completion takes about 335 cycles to be seen, a barrier about 100): with one buffer of
 // 128 keys a tile, kernels with a quarter of the products and no exponentials took 70 % of
 // the time.  Two tiles x two buffers keep four chains in flight.
-// 16 heads of 128, window 2048, 4 sinks: 1 x 4096 87 us, 1 x 16384 312 us (828 TFLOP/s, the
-// tensor pipe active 39 % of the time); 8192 causal over 4 key heads 270 us (1017 TFLOP/s).
+// 16 heads of 128, window 2048, 4 sinks: 1 x 4096 82 to 85 us, 1 x 16384 302 to 316 us (about
+// 840 TFLOP/s, the tensor pipe active 40 % of the time); heads of 64: 75 and 283 us.
 //
 // CTAs are persistent: a CTA that finishes asks the hardware for a block that has not
 // started (cluster launch control) and runs it, so the next rows' loads and first scores

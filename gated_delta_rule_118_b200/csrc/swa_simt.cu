@@ -3,9 +3,11 @@
 // tiles).  The products are 64-wide register tiles over shared memory; bound by
 // the FFMA rate (every score costs 2 d FMAs, and the two-kernel backward forms
 // q k^T and dO v^T twice in exchange for a fixed order of every sum).  3 x 333 x 6 heads
-// of 64 over 2, window 100, forward and backward: 125 us in five launches, each a fraction
+// of 64 over 2, window 100, forward and backward: 121 us in five launches, each a fraction
 // of a wave, so bound by the walk of one CTA; 2 x 4096 x 8 heads of 64, window 512: forward
-// 342 us, backward 2016, a quarter of the FFMA rate, for the barriers between a tile's steps.
+// 342 us, backward 2010, a third and a fifth of the FFMA rate: a dot product's register tile
+// of 4 x 4 reads shared memory for three quarters of its FMAs' cycles, the backward's of 4 x 2
+// and 2 x 4 for as many cycles as its FMAs, and three to five barriers a tile stand between.
 #include "launch.h"
 #include "swa_common.cuh"
 
