@@ -18,11 +18,11 @@
 // the way out.
 //
 // Bound by the tensor pipe and the hand-overs around it: 4 x 4096, 16 query heads of 128
-// over 4, window 2048, 4 sinks: 890 to 980 us with the clock the device holds, dk and dv
-// a little more of it than dq (tensor pipe active 60 % and 52 % of the time); 1 x 16384 x 16
-// heads 1160 to 1320 us.  One thread issues the
-// products of dk and dv (with a warp for those of P and one for those of dS 1224 us against
-// 1197: each delays the other's), and one each those of scores and of dq (1197 against 1222).
+// over 4, window 2048, 4 sinks: 890 to 980 us from one device to another, dk and dv a little
+// more of it than dq (tensor pipe active 60 % and 52 % of the time); 1 x 16384 x 16 heads 1160
+// to 1320 us.  One thread issues the products of dk and dv (with a warp for those of P and one
+// for those of dS 1224 us against 1197: each delays the other's), and one each those of scores
+// and of dq (1197 against 1222).
 //
 // Keys that every later row sees (sinks) have as many query tiles as the sequence;
 // where that would leave a few CTAs with most of the work, their query range is split

@@ -13,7 +13,8 @@
 // 128 keys a tile, kernels with a quarter of the products and no exponentials took 70 % of
 // the time.  Two tiles x two buffers keep four chains in flight.
 // 16 heads of 128, window 2048, 4 sinks: 1 x 4096 82 to 85 us, 1 x 16384 302 to 316 us (about
-// 840 TFLOP/s, the tensor pipe active 40 % of the time); heads of 64: 75 and 283 us.
+// 840 TFLOP/s, the tensor pipe active 40 % of the time); heads of 64: 75 and 283 us; 8192
+// causal, 16 heads of 128 over 4, 270 us (1017 TFLOP/s).
 //
 // CTAs are persistent: a CTA that finishes asks the hardware for a block that has not
 // started (cluster launch control) and runs it, so the next rows' loads and first scores
